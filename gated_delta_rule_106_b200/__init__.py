@@ -14,9 +14,11 @@ Agnes-3.0-Flash Preview model card, 架构 table (gated RMS-norm).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -30,10 +32,13 @@ __all__ = ["GDN_BF16", "GDN_F32", "GdnError", "library_path", "load",
            "gdn_gated_rmsnorm", "gdn_status_string", "gdn_version",
            "gdn_attention_prefill", "gdn_attention_decode", "gdn_attention_status",
            "ATTN_H_Q", "ATTN_H_KV", "ATTN_HEAD_DIM",
+           "GDN_F16", "PagePlan", "gdn_page_plan", "gdn_rope_inv_freq", "gdn_qk_norm_rope",
+           "gdn_paged_attention_decode", "gdn_paged_attention_decode_workspace",
            "H_K", "H_V", "HEAD_DIM", "CHUNK"]
 
 GDN_BF16 = 0
 GDN_F32 = 1
+GDN_F16 = 2
 GDN_ERR_TIMEOUT = -5
 H_K, H_V, HEAD_DIM, CHUNK = 16, 48, 128, 64
 
@@ -46,6 +51,7 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 # name -> (restype, argtypes)
 _SIGNATURES = {
@@ -58,6 +64,18 @@ _SIGNATURES = {
                                     _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _int,
                                     _f32, _int, _f32, _f32, _vp, _vp, ctypes.c_size_t, _vp]),
     "gdn_attention_status": (_int, [_vp, _vp]),
+    "gdn_page_plan": (_int, [_vp, _vp, _int, _vp, _i64, _int, _vp, _vp, _int, _int, _i64,
+                             _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "gdn_rope_inv_freq": (_int, [_int, _f64, _f64, _f64, _f64, _f64, _vp, _vp]),
+    "gdn_qk_norm_rope": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _vp, _int, _f32,
+                                _vp, _int, _vp, _int, _int, _f32, _vp, _i64, _int, _int, _int,
+                                _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _int, _int,
+                                _int, _vp]),
+    "gdn_paged_attention_decode_workspace": (ctypes.c_size_t, [_int, _int, _int]),
+    "gdn_paged_attention_decode": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64,
+                                          _i64, _int, _int, _int, _vp, _i64, _int, _vp, _vp,
+                                          _i64, _int, _int, _int, _int, _f32, _vp, _int, _vp,
+                                          _vp, ctypes.c_size_t, _vp]),
     "gdn_status_string": (ctypes.c_char_p, [_int]),
     "gdn_version": (ctypes.c_char_p, []),
     "gdn_conv1d_silu": (_int, [_vp, _i64, _int, _vp, _int, _vp, _int, _int, _f32,
@@ -524,3 +542,265 @@ def gdn_attention_status(workspace, stream=None) -> int:
     sequence with an out-of-range slot or length)."""
     return int(load().gdn_attention_status(_ptr(workspace), _stream(stream, workspace.device)))
 
+
+
+# ------------------------------------------------------------------ paged cache
+_DTYPE3 = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float16: GDN_F16}
+_HERE_NOW = contextlib.nullcontext()
+
+
+def _dtype3(t: torch.dtype, name) -> int:
+    code = _DTYPE3.get(t)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t}; use torch.bfloat16, float16 or float32")
+    return code
+
+
+def _one_device(*tensors):
+    """The CUDA device that all given tensors are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libgdn takes CUDA tensors only (no CPU path)")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    return dev
+
+
+def _on(dev, stream):
+    """Makes `dev` and `stream` current for the allocations and the launch of a
+    call, so that buffers made for it belong to the stream that uses them."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return _HERE_NOW
+
+
+def _rows32(t, name, shape=None):
+    """Pointer and row stride of an int32 [N, M] tensor with dense rows."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape or '[N, max_pages]'}")
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]     # one row: no stride is used
+
+
+def _cache_strides(t, name, shape=None, dtype=None):
+    """(page, token, head) strides of a [pages, page_size, H_kv, D] cache view."""
+    if t.dim() != 4 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
+                         f"{shape or '[num_pages, page_size, H_kv, D]'}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    D = t.shape[3]
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: each row of {D} values must be contiguous")
+    # the stride of a dimension of one is never used
+    return [t.stride(i) if t.shape[i] > 1 else D for i in range(3)]
+
+
+def _head_rows3(t, shape, name, dtype):
+    _expect(t, shape, name, dtype, contiguous=False)
+    stride = _row_stride(t)
+    return stride if t.shape[0] > 1 else shape[1] * shape[2]
+
+
+class PagePlan(NamedTuple):
+    """What gdn_page_plan returns: lengths after the step [N]; prefix sums of the
+    new tokens [N+1]; slot and position of each new token [token_capacity]; the
+    filled entries of the free stack [1]; (new tokens, pages taken, pages
+    returned, requests refused)."""
+    new_lens: torch.Tensor
+    cu_new: torch.Tensor
+    slot_map: torch.Tensor
+    positions: Optional[torch.Tensor]
+    new_count: torch.Tensor
+    info: Optional[torch.Tensor]
+
+
+def gdn_page_plan(lens, want, block_table, free_pages, free_count, page_size, *,
+                  token_capacity=None, new_lens=None, cu_new=None, slot_map=None, positions=None,
+                  new_count=None, info=None, stream=None):
+    """Moves requests from lens [N] to want [N] tokens (int32; 0 releases):
+    writes the new entries of block_table [N, max_pages], returns pages to and
+    takes pages from the stack free_pages [num_pages] with free_count [1]
+    entries, and gives every new token its cache slot and position
+    (token_capacity entries; -1 and 0 behind the last). Growth that does not fit
+    is refused from the first such request on. lens, want and free_count stay as
+    they are: adopt new_lens and new_count to go on. Returns a PagePlan."""
+    N, P = lens.numel(), free_pages.numel()
+    if slot_map is not None:
+        if token_capacity not in (None, slot_map.numel()):
+            raise ValueError("token_capacity is not slot_map's length")
+        token_capacity = slot_map.numel()
+    if token_capacity is None:
+        raise ValueError("give token_capacity or slot_map")
+    i32 = torch.int32
+    _expect(lens, (N,), "lens", i32)
+    _expect(want, (N,), "want", i32)
+    row = _rows32(block_table, "block_table", (N, block_table.shape[-1]))
+    _expect(free_pages, (P,), "free_pages", i32)
+    _expect(free_count, (1,), "free_count", i32)
+    _expect(new_lens, (N,), "new_lens", i32)
+    _expect(cu_new, (N + 1,), "cu_new", i32)
+    _expect(slot_map, (token_capacity,), "slot_map", i32)
+    _expect(positions, (token_capacity,), "positions", i32)
+    _expect(new_count, (1,), "new_count", i32)
+    _expect(info, (4,), "info", i32)
+    dev = _one_device(lens, want, block_table, free_pages, free_count, new_lens, cu_new, slot_map,
+                      positions, new_count, info)
+    with _on(dev, stream):
+        def buf(t, n):
+            return torch.empty(n, dtype=i32, device=dev) if t is None else t
+        out = PagePlan(buf(new_lens, N), buf(cu_new, N + 1), buf(slot_map, token_capacity),
+                       buf(positions, token_capacity), buf(new_count, 1), buf(info, 4))
+        _check("gdn_page_plan", load().gdn_page_plan(
+            lens.data_ptr(), want.data_ptr(), N, block_table.data_ptr(), row,
+            block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(), P, page_size,
+            token_capacity, *(t.data_ptr() for t in out), _stream(None, dev)))
+    return out
+
+
+def gdn_rope_inv_freq(rope_dims, base=1e7, *, factor=1.0, context=0, beta_fast=32.0,
+                      beta_slow=1.0, out=None, device=None, stream=None):
+    """Rotary frequencies base^(-2i / rope_dims) in fp64 [rope_dims / 2] for
+    gdn_qk_norm_rope, all divided by `factor`, or with `context` (the trained
+    length) by parts: pairs that turn often over it keep their frequency."""
+    if out is None:
+        out = torch.empty(rope_dims // 2, dtype=torch.float64,
+                          device="cuda" if device is None else device)
+    _expect(out, (rope_dims // 2,), "out", torch.float64)
+    dev = _one_device(out)
+    with _on(dev, stream):
+        _check("gdn_rope_inv_freq", load().gdn_rope_inv_freq(
+            rope_dims, base, factor, context, beta_fast, beta_slow, out.data_ptr(),
+            _stream(None, dev)))
+    return out
+
+
+def gdn_qk_norm_rope(q, k, v, k_cache=None, v_cache=None, *, slot_map=None, q_norm_w=None,
+                     k_norm_w=None, positions=None, inv_freq=None, interleaved=False,
+                     rope_scale=1.0, eps=1e-6, q_out=None, out_dtype=None, stream=None):
+    """Per-head RMS-norm (where a weight [D] is given) and rotary (where inv_freq,
+    fp64 [rope_dims / 2], is given; positions int32 [T] or [3, T]) of q [T, H_q,
+    D] and k [T, H_kv, D], and the append of k and v to the paged caches
+    [num_pages, page_size, H_kv, D] (strided views; bf16 or fp16) at slot_map [T]
+    (a slot outside the cache marks padding; None: token t at slot t). q, or k
+    and v, may be None. Returns q_out [T, H_q, D] in the caches' dtype."""
+    x = q if q is not None else k
+    if x is None or (k is None) != (v is None) or (k is None) != (k_cache is None) or \
+            (k is None) != (v_cache is None):
+        raise ValueError("give q, or k and v with both caches, or all")
+    if x.dim() != 3:
+        raise ValueError(f"q, k, v: {x.dim()} dimensions, expected [T, H, D]")
+    T, D = x.shape[0], x.shape[2]
+    H_q = q.shape[1] if q is not None else 0
+    H_kv = k.shape[1] if k is not None else 0
+    P = page = ks = vs = 0
+    k_str = v_str = (0, 0, 0)
+    if k is not None:
+        ks = _head_rows3(k, (T, H_kv, D), "k", x.dtype)
+        vs = _head_rows3(v, (T, H_kv, D), "v", x.dtype)
+        P, page = k_cache.shape[0], k_cache.shape[1]
+        k_str = _cache_strides(k_cache, "k_cache", (P, page, H_kv, D))
+        v_str = _cache_strides(v_cache, "v_cache", (P, page, H_kv, D), k_cache.dtype)
+        if out_dtype not in (None, k_cache.dtype):
+            raise ValueError(f"out_dtype {out_dtype}: q_out has the caches' dtype")
+        out_dtype = k_cache.dtype
+    elif out_dtype is None:
+        out_dtype = q_out.dtype if q_out is not None else torch.float16
+    if out_dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"caches and q_out are bf16 or fp16, got {out_dtype}")
+    qs = _head_rows3(q, (T, H_q, D), "q", x.dtype) if q is not None else 0
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    _expect(q_out, (T, H_q, D), "q_out", out_dtype)
+    w = q_norm_w if q_norm_w is not None else k_norm_w
+    _expect(q_norm_w, (D,), "q_norm_w", None)
+    _expect(k_norm_w, (D,), "k_norm_w", None if w is None else w.dtype)
+    _expect(slot_map, (T,), "slot_map", torch.int32)
+    R, axes = 0, 1
+    if inv_freq is not None:
+        R = 2 * inv_freq.numel()
+        _expect(inv_freq, (R // 2,), "inv_freq", torch.float64)
+        if positions is None:
+            raise ValueError("rotary needs positions")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        _expect(positions, (T,) if positions.dim() == 1 else (3, T), "positions", torch.int32)
+    elif positions is not None:
+        raise ValueError("positions without inv_freq")
+    dev = _one_device(q, k, v, k_cache, v_cache, slot_map, q_norm_w, k_norm_w, positions,
+                      inv_freq, q_out)
+    xd = _dtype3(x.dtype, "q, k, v")
+    wd = GDN_F32 if w is None else _dtype3(w.dtype, "norm weights")
+    with _on(dev, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty((T, H_q, D), dtype=out_dtype, device=dev)
+        _check("gdn_qk_norm_rope", load().gdn_qk_norm_rope(
+            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, xd, _ptr(q_norm_w), _ptr(k_norm_w), wd, eps,
+            _ptr(positions), axes, _ptr(inv_freq), R, int(bool(interleaved)), rope_scale,
+            _ptr(slot_map), T, H_q, H_kv, D, _ptr(q_out), _ptr(k_cache), *k_str, _ptr(v_cache),
+            *v_str, P, page, _DTYPE3[out_dtype], _stream(None, dev)))
+    return q_out
+
+
+def gdn_paged_attention_decode_workspace(H_q, H_kv, head_dim=ATTN_HEAD_DIM) -> int:
+    """Bytes of workspace gdn_paged_attention_decode needs (any N, any lengths)."""
+    return int(load().gdn_paged_attention_decode_workspace(H_q, H_kv, head_dim))
+
+
+def gdn_paged_attention_decode(q, k_cache, v_cache, block_table, kv_lens, *, gate=None,
+                               scale=None, o=None, o_dtype=None, lse=None, workspace=None,
+                               stream=None):
+    """Attention of one query token per sequence, q [N, H_q, D] (the caches'
+    dtype, any row stride), over kv_lens [N] cached tokens of the paged caches
+    [num_pages, page_size, H_kv, D] (strided views) through block_table [N,
+    max_pages] (int32). gate [N, H_q, D] bf16: times sigmoid(gate). lse [N, H_q]
+    fp32 receives the log of the softmax sums. Returns o [N, H_q, D] (o_dtype,
+    bf16 unless given). A sequence of length 0 gives zeros."""
+    if q.dim() != 3:
+        raise ValueError(f"q: {q.dim()} dimensions, expected [N, H_q, D]")
+    N, H_q, D = q.shape
+    k_str = _cache_strides(k_cache, "k_cache")
+    P, page, H_kv, _ = k_cache.shape
+    if k_cache.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"caches are bf16 or fp16, got {k_cache.dtype}")
+    v_str = _cache_strides(v_cache, "v_cache", (P, page, H_kv, D), k_cache.dtype)
+    if k_cache.shape[3] != D:
+        raise ValueError(f"k_cache: head dim {k_cache.shape[3]}, q has {D}")
+    qs = _head_rows3(q, (N, H_q, D), "q", k_cache.dtype)
+    row = _rows32(block_table, "block_table", (N, block_table.shape[-1]))
+    _expect(kv_lens, (N,), "kv_lens", torch.int32)
+    gs = 0
+    if gate is not None:
+        gs = _head_rows3(gate, (N, H_q, D), "gate", torch.bfloat16)
+    _expect(o, (N, H_q, D), "o")
+    _expect(lse, (N, H_q), "lse", torch.float32)
+    if o is None:
+        o_dtype = o_dtype or torch.bfloat16
+    elif o_dtype not in (None, o.dtype):
+        raise ValueError(f"o: dtype {o.dtype}, expected {o_dtype}")
+    od = _dtype3(o_dtype if o is None else o.dtype, "o")
+    dev = _one_device(q, k_cache, v_cache, block_table, kv_lens, gate, o, lse, workspace)
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty((N, H_q, D), dtype=o_dtype, device=dev)
+        if workspace is None:
+            workspace = torch.empty(
+                max(gdn_paged_attention_decode_workspace(H_q, H_kv, D), 256),
+                dtype=torch.uint8, device=dev)
+        _check("gdn_paged_attention_decode", load().gdn_paged_attention_decode(
+            _ptr(q), qs, _ptr(k_cache), *k_str, _ptr(v_cache), *v_str, _DTYPE3[k_cache.dtype],
+            P, page, _ptr(block_table), row, block_table.shape[1], _ptr(kv_lens), _ptr(gate), gs,
+            N, H_q, H_kv, D, D ** -0.5 if scale is None else scale, _ptr(o), od, _ptr(lse),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(None, dev)))
+    return o

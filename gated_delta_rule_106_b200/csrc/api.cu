@@ -445,6 +445,197 @@ gdn_status gdn_attention_decode(const void* q, int64_t q_row_stride, const void*
   return from_cuda(gdn::launch_attention_decode(a));
 }
 
+// ------------------------------------------------------------ paged cache
+
+namespace {
+
+bool valid_dtype3(gdn_dtype t) { return valid_dtype(t) || t == GDN_F16; }
+bool half_dtype(gdn_dtype t) { return t == GDN_F16 || t == GDN_BF16; }
+bool paged_dim(int d) { return d == 64 || d == 128 || d == 256; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
+// a cache and its strides: rows of D values, 16-byte aligned, inside int32 slots
+gdn_status check_cache(const void* base, const gdn::PageStrides& s, int num_pages, int page_size,
+                       int D) {
+  if (!base || num_pages <= 0 || page_size <= 0) return GDN_ERR_INVALID_ARG;
+  if ((int64_t)num_pages * page_size > INT32_MAX) return GDN_ERR_INVALID_ARG;
+  if (s.page < 0 || s.token < 0 || s.head < 0) return GDN_ERR_INVALID_ARG;
+  if ((num_pages > 1 && s.page < D) || (page_size > 1 && s.token < D) || s.head < D)
+    return GDN_ERR_INVALID_ARG;
+  if (!aligned16(base) || s.page % 8 != 0 || s.token % 8 != 0 || s.head % 8 != 0)
+    return GDN_ERR_MISALIGNED;
+  return GDN_OK;
+}
+
+}  // namespace
+
+gdn_status gdn_page_plan(const int32_t* lens, const int32_t* want, int N,
+                         int32_t* block_table, int64_t table_row_stride, int max_pages,
+                         int32_t* free_pages, const int32_t* free_count, int num_pages,
+                         int page_size, int64_t token_capacity, int32_t* new_lens,
+                         int32_t* cu_new, int32_t* slot_map, int32_t* positions,
+                         int32_t* new_count, int32_t* info, cudaStream_t stream) {
+  if (N < 0 || max_pages <= 0 || num_pages <= 0 || page_size <= 0 || token_capacity < 0 ||
+      token_capacity > (int64_t)1 << 30 || table_row_stride < max_pages)
+    return GDN_ERR_INVALID_ARG;
+  if (N > gdn::kPlanMaxRequests) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)num_pages * page_size > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX ||
+      num_pages > 1 << 30 || (int64_t)N * max_pages > INT32_MAX)
+    return GDN_ERR_INVALID_ARG;
+  if (!free_pages || !free_count || !cu_new || !new_count || (token_capacity > 0 && !slot_map))
+    return GDN_ERR_INVALID_ARG;
+  if (N > 0 && (!lens || !want || !block_table || !new_lens)) return GDN_ERR_INVALID_ARG;
+  const struct { const void* p; size_t n; } in[] = {
+      {lens, (size_t)N * 4}, {want, (size_t)N * 4}, {free_count, 4}},
+      out[] = {{new_lens, (size_t)N * 4}, {cu_new, (size_t)(N + 1) * 4},
+               {slot_map, (size_t)token_capacity * 4}, {positions, (size_t)token_capacity * 4},
+               {new_count, 4}, {info, 16}, {free_pages, (size_t)num_pages * 4},
+               {block_table, N > 0 ? ((size_t)(N - 1) * table_row_stride + max_pages) * 4 : 0}};
+  for (const auto& a : in)
+    if (!aligned_to(a.p, 4)) return GDN_ERR_MISALIGNED;
+  for (const auto& a : out)
+    if (!aligned_to(a.p, 4)) return GDN_ERR_MISALIGNED;
+  if (!aligned16(slot_map) || !aligned16(positions)) return GDN_ERR_MISALIGNED;
+  const int outs = (int)(sizeof(out) / sizeof(out[0]));
+  for (int i = 0; i < outs; ++i) {
+    for (const auto& b : in)
+      if (overlap(out[i].p, out[i].n, b.p, b.n)) return GDN_ERR_INVALID_ARG;
+    for (int j = i + 1; j < outs; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return GDN_ERR_INVALID_ARG;
+  }
+  gdn::PagePlanArgs a{lens, want, N, block_table, table_row_stride, max_pages, free_pages,
+                      free_count, num_pages, page_size, token_capacity, new_lens, cu_new,
+                      slot_map, positions, new_count, info, stream};
+  return from_cuda(gdn::launch_page_plan(a));
+}
+
+gdn_status gdn_rope_inv_freq(int rope_dims, double base, double factor, double context,
+                             double beta_fast, double beta_slow, double* out,
+                             cudaStream_t stream) {
+  if (rope_dims < 0 || rope_dims % 2 != 0 || rope_dims > 256) return GDN_ERR_UNSUPPORTED;
+  if (!(base > 1.0) || !(factor >= 1.0) || !(context >= 0.0) ||
+      (context > 0.0 && !(beta_fast > beta_slow)))
+    return GDN_ERR_INVALID_ARG;
+  if (rope_dims == 0) return GDN_OK;
+  if (!out) return GDN_ERR_INVALID_ARG;
+  if (!aligned_to(out, 8)) return GDN_ERR_MISALIGNED;
+  return from_cuda(gdn::launch_rope_inv_freq(rope_dims, base, factor, context, beta_fast,
+                                             beta_slow, out, stream));
+}
+
+gdn_status gdn_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k,
+                            int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                            gdn_dtype x_dtype, const void* q_norm_w, const void* k_norm_w,
+                            gdn_dtype w_dtype, float eps, const int32_t* positions, int axes,
+                            const double* inv_freq, int rope_dims, int interleaved,
+                            float rope_scale, const int32_t* slot_map, int64_t T, int H_q,
+                            int H_kv, int head_dim, void* q_out, void* k_cache,
+                            int64_t k_page_stride, int64_t k_token_stride,
+                            int64_t k_head_stride, void* v_cache, int64_t v_page_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, int num_pages,
+                            int page_size, gdn_dtype out_dtype, cudaStream_t stream) {
+  if (!paged_dim(head_dim)) return GDN_ERR_UNSUPPORTED;
+  if (rope_dims < 0 || rope_dims % 2 != 0 || rope_dims > head_dim) return GDN_ERR_UNSUPPORTED;
+  if (!half_dtype(out_dtype)) return GDN_ERR_UNSUPPORTED;
+  if (!valid_dtype3(x_dtype) || !valid_dtype3(w_dtype) || !(eps >= 0.f) || T < 0 ||
+      T > (int64_t)1 << 30)
+    return GDN_ERR_INVALID_ARG;
+  if ((!q && !k) || (!k) != (!v)) return T == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
+  if ((q && (H_q <= 0 || H_q > 1 << 16)) || (k && (H_kv <= 0 || H_kv > 1 << 16)))
+    return GDN_ERR_INVALID_ARG;
+  if (rope_dims > 0 && axes != 1 && axes != 3) return GDN_ERR_INVALID_ARG;
+  const int64_t q_row = (int64_t)H_q * head_dim, kv_row = (int64_t)H_kv * head_dim;
+  if ((q && q_row_stride < q_row) || (k && (k_row_stride < kv_row || v_row_stride < kv_row)))
+    return GDN_ERR_INVALID_ARG;
+  if ((q && !stride_ok(q_row_stride, x_dtype)) ||
+      (k && (!stride_ok(k_row_stride, x_dtype) || !stride_ok(v_row_stride, x_dtype))))
+    return GDN_ERR_MISALIGNED;
+  const gdn::PageStrides ks{k_page_stride, k_token_stride, k_head_stride},
+      vs{v_page_stride, v_token_stride, v_head_stride};
+  if (k) {
+    gdn_status st = check_cache(k_cache, ks, num_pages, page_size, head_dim);
+    if (st == GDN_OK) st = check_cache(v_cache, vs, num_pages, page_size, head_dim);
+    if (st != GDN_OK) return st;
+    if (!slot_map && T > (int64_t)num_pages * page_size) return GDN_ERR_INVALID_ARG;
+  }
+  if (T == 0) return GDN_OK;
+  if ((q && !q_out) || (rope_dims > 0 && (!positions || !inv_freq))) return GDN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || (q && !aligned16(q_out)))
+    return GDN_ERR_MISALIGNED;
+  const int wb = gdn::elem_bytes(w_dtype);
+  if (!aligned_to(q_norm_w, wb) || !aligned_to(k_norm_w, wb) || !aligned_to(positions, 4) ||
+      !aligned_to(inv_freq, 8) || !aligned_to(slot_map, 4))
+    return GDN_ERR_MISALIGNED;
+  if (q) {
+    const size_t xb = (size_t)gdn::elem_bytes(x_dtype);
+    const size_t in = ((size_t)(T - 1) * q_row_stride + q_row) * xb;
+    const size_t out = (size_t)T * q_row * 2;
+    const bool same = q == q_out && x_dtype == out_dtype && q_row_stride == q_row;
+    if (!same && overlap(q, in, q_out, out)) return GDN_ERR_INVALID_ARG;
+    if (k) {
+      const size_t kn = ((size_t)(T - 1) * k_row_stride + kv_row) * xb;
+      const size_t vn = ((size_t)(T - 1) * v_row_stride + kv_row) * xb;
+      if (overlap(k, kn, q_out, out) || overlap(v, vn, q_out, out)) return GDN_ERR_INVALID_ARG;
+    }
+  }
+  gdn::NormRopeArgs a{q, k, v, q_row_stride, k_row_stride, v_row_stride, x_dtype, q_norm_w,
+                      k_norm_w, w_dtype, eps, positions, axes, inv_freq, rope_dims, interleaved,
+                      rope_scale, slot_map, T, H_q, H_kv, head_dim, q_out, k_cache, v_cache, ks,
+                      vs, num_pages, page_size, out_dtype, stream};
+  return from_cuda(gdn::launch_qk_norm_rope(a));
+}
+
+size_t gdn_paged_attention_decode_workspace(int H_q, int H_kv, int head_dim) {
+  if (H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || !paged_dim(head_dim)) return 0;
+  return gdn::paged_decode_workspace(H_q / H_kv, head_dim);
+}
+
+gdn_status gdn_paged_attention_decode(const void* q, int64_t q_row_stride, const void* k_cache,
+                                      int64_t k_page_stride, int64_t k_token_stride,
+                                      int64_t k_head_stride, const void* v_cache,
+                                      int64_t v_page_stride, int64_t v_token_stride,
+                                      int64_t v_head_stride, gdn_dtype kv_dtype, int num_pages,
+                                      int page_size, const int32_t* block_table,
+                                      int64_t table_row_stride, int max_pages,
+                                      const int32_t* kv_lens, const void* gate,
+                                      int64_t gate_row_stride, int N, int H_q, int H_kv,
+                                      int head_dim, float scale, void* o, gdn_dtype o_dtype,
+                                      float* lse, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream) {
+  if (!paged_dim(head_dim) || !half_dtype(kv_dtype)) return GDN_ERR_UNSUPPORTED;
+  if (H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || H_q > 65535 || N < 0 || N > 65535 ||
+      !valid_dtype3(o_dtype) || !(scale == scale))
+    return GDN_ERR_INVALID_ARG;
+  if (H_q / H_kv > 16) return GDN_ERR_UNSUPPORTED;
+  const int64_t row = (int64_t)H_q * head_dim;
+  if (q_row_stride < row || (gate && gate_row_stride < row) || max_pages <= 0 ||
+      table_row_stride < max_pages || (int64_t)max_pages * page_size > INT32_MAX)
+    return GDN_ERR_INVALID_ARG;
+  const gdn::PageStrides ks{k_page_stride, k_token_stride, k_head_stride},
+      vs{v_page_stride, v_token_stride, v_head_stride};
+  gdn_status st = check_cache(k_cache, ks, num_pages, page_size, head_dim);
+  if (st == GDN_OK) st = check_cache(v_cache, vs, num_pages, page_size, head_dim);
+  if (st != GDN_OK) return st;
+  if (N == 0) return GDN_OK;
+  if (!q || !block_table || !kv_lens || !o || !workspace) return GDN_ERR_INVALID_ARG;
+  if (workspace_bytes < gdn::paged_decode_workspace(H_q / H_kv, head_dim))
+    return GDN_ERR_INVALID_ARG;
+  if (!aligned16(q) || q_row_stride % 8 != 0 || !aligned16(gate) ||
+      (gate && gate_row_stride % 8 != 0) || !aligned16(o) || !aligned16(workspace) ||
+      !aligned_to(block_table, 4) || !aligned_to(kv_lens, 4) || !aligned_to(lse, 4))
+    return GDN_ERR_MISALIGNED;
+  gdn::PagedDecodeArgs a{q, q_row_stride, k_cache, v_cache, ks, vs, kv_dtype, num_pages,
+                         page_size, block_table, table_row_stride, max_pages, kv_lens, gate,
+                         gate_row_stride, N, H_q, H_kv, head_dim, scale, o, o_dtype, lse,
+                         workspace, stream};
+  return from_cuda(gdn::launch_paged_decode(a));
+}
+
 gdn_status gdn_attention_status(const void* workspace, cudaStream_t stream) {
   if (!workspace) return GDN_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return GDN_ERR_MISALIGNED;

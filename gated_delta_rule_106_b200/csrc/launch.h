@@ -99,6 +99,46 @@ struct AttnDecodeArgs {
   cudaStream_t stream;
 };
 
+// Page plan: block tables, free stack, slots and positions from request lengths.
+constexpr int kPlanMaxRequests = 16384;   // running sums of 3 x 4 bytes each in shared memory
+struct PagePlanArgs {
+  const int32_t* lens; const int32_t* want; int N;
+  int32_t* table; int64_t table_row_stride; int max_pages;
+  int32_t* free_pages; const int32_t* free_count; int num_pages; int page_size;
+  int64_t token_capacity;
+  int32_t* new_lens; int32_t* cu_new; int32_t* slot_map; int32_t* positions;
+  int32_t* new_count; int32_t* info;
+  cudaStream_t stream;
+};
+
+// Strides (elements) of a paged cache [pages, page_size, heads, head_dim].
+struct PageStrides { int64_t page, token, head; };
+
+// q/k norm + rotary + append of k and v to a paged cache.
+struct NormRopeArgs {
+  const void* q; const void* k; const void* v; int64_t q_row_stride, k_row_stride, v_row_stride;
+  gdn_dtype x_dtype;
+  const void* q_norm_w; const void* k_norm_w; gdn_dtype w_dtype; float eps;
+  const int32_t* positions; int axes; const double* inv_freq; int rope_dims; int interleaved;
+  float rope_scale;
+  const int32_t* slot_map; int64_t T; int Hq, Hkv, D;
+  void* q_out; void* k_cache; void* v_cache; PageStrides ks, vs; int num_pages, page_size;
+  gdn_dtype out_dtype;
+  cudaStream_t stream;
+};
+
+// One-token attention over a paged cache.
+struct PagedDecodeArgs {
+  const void* q; int64_t q_row_stride;
+  const void* k_cache; const void* v_cache; PageStrides ks, vs; gdn_dtype kv_dtype;
+  int num_pages, page_size;
+  const int32_t* table; int64_t table_row_stride; int max_pages; const int32_t* kv_lens;
+  const void* gate; int64_t gate_row_stride;
+  int N, Hq, Hkv, D; float scale;
+  void* o; gdn_dtype o_dtype; float* lse; void* workspace;
+  cudaStream_t stream;
+};
+
 struct NormArgs {
   const void* x; gdn_dtype x_dtype; const void* z; gdn_dtype z_dtype;
   const void* w; gdn_dtype w_dtype; int64_t rows; int dim; float eps;
@@ -133,6 +173,13 @@ cudaError_t launch_attention_prefill(const AttnPrefillArgs& a);
 size_t attention_prefill_workspace(int64_t T, int Hq);
 cudaError_t launch_attention_decode(const AttnDecodeArgs& a);
 size_t attention_decode_workspace(int N, int Hq, int L_max);
+cudaError_t launch_page_plan(const PagePlanArgs& a);
+cudaError_t launch_rope_inv_freq(int rope_dims, double base, double factor, double context,
+                                 double beta_fast, double beta_slow, double* out,
+                                 cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(const NormRopeArgs& a);
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a);
+size_t paged_decode_workspace(int group, int D);
 // Synchronises `stream`, then reads the status word the last attention call
 // left in `workspace` (1: a wait inside the kernel ran out).
 cudaError_t attention_status_word(const void* workspace, cudaStream_t stream, int* word);

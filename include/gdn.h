@@ -62,7 +62,11 @@ typedef enum {
   GDN_ERR_TIMEOUT = -5      /* a bounded wait inside a kernel gave up      */
 } gdn_status;
 
-typedef enum { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
+typedef enum {
+  GDN_BF16 = 0,
+  GDN_F32 = 1,
+  GDN_F16 = 2 /* paged-cache entry points only; the others refuse it */
+} gdn_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* gdn_status_string(gdn_status status);
@@ -452,6 +456,163 @@ gdn_status gdn_attention_decode(const void* q, int64_t q_row_stride, const void*
  * a decode sequence had an out-of-range slot or length. Additional entry point.
  */
 gdn_status gdn_attention_status(const void* workspace, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key-value cache: the global-attention layer's cache cut into pages
+ * that requests of any length share, for serving many requests at once. A
+ * step of a server is
+ *   gdn_page_plan               lengths -> block table, slots, positions
+ *   gdn_qk_norm_rope            q/k norm + rotary, k and v into their slots
+ *   gdn_paged_attention_decode  one new token per sequence over its pages
+ * A cache is [num_pages, page_size, H_kv, head_dim] seen through strides
+ * (elements) per page, token and head, multiples of 8, each row of head_dim
+ * values contiguous: tokens before heads, heads before tokens, or both caches
+ * in one buffer. head_dim is 64, 128 or 256. Slot s of a cache is offset
+ * s % page_size of page s / page_size. num_pages * page_size and
+ * max_pages * page_size are below 2^31; element offsets are 64-bit.
+ * These entry points are additional (the pages name the layer, no cache
+ * layout). No gradient: the library serves.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * gdn_page_plan -- moves N requests from lens[n] to want[n] tokens: block-table
+ * entries, the stack of free pages, a cache slot and a position for every new
+ * token, in one launch without a host round trip. With held[n] =
+ * ceil(lens[n] / page_size) and goal[n] = ceil(want[n] / page_size):
+ *   want < lens   shrinks (0 releases the request): entries goal..held-1 of its
+ *                 table row return to the stack, in request order;
+ *   want > lens   grows: after all returns, requests take goal - held pages
+ *                 from the stack's top, in request order. The first growing
+ *                 request whose pages or tokens no longer fit, and every
+ *                 growing request after it, is refused and stays at lens[n];
+ *   a length outside [0, max_pages * page_size] refuses its request alone.
+ *
+ *   lens, want   [N] int32.
+ *   block_table  [N, max_pages] int32, row stride table_row_stride: entries
+ *                held..goal-1 of granted rows are written, all others are left
+ *                as they were (returned entries too).
+ *   free_pages   [num_pages] int32 stack of which free_count[0] (clamped into
+ *                [0, num_pages]) entries are filled; returned pages are written
+ *                behind them, except those that are taken again at once.
+ *                Returns past num_pages entries are dropped.
+ *   token_capacity  room for new tokens, up to 2^30.
+ *   new_lens     [N] want[n], or lens[n] where refused.
+ *   cu_new       [N+1] prefix sums of the granted new tokens.
+ *   slot_map, positions  [token_capacity]: new token i of request n at index
+ *                cu_new[n] + i has position lens[n] + i and its slot; entries
+ *                past the last new token get slot -1 and position 0, so a step
+ *                of fixed size can be captured once. A table or stack entry
+ *                outside [0, num_pages) gives slot -1.
+ *   new_count    [1] filled entries of the stack afterwards.
+ *   info         [4] or NULL: new tokens, pages taken, pages returned, requests
+ *                refused.
+ * positions may be NULL, slot_map too when token_capacity is 0. slot_map and
+ * positions are 16-byte aligned, the other arrays 4-byte. The outputs must not
+ * overlap the inputs or one another: the inputs stay as they are, so the same
+ * call again gives the same result, and a plan that is not adopted costs
+ * nothing but the table and stack entries past the old lengths. Two rows must
+ * not hold the same page if either returns it. N is at most 16384
+ * (GDN_ERR_UNSUPPORTED).
+ */
+gdn_status gdn_page_plan(const int32_t* lens, const int32_t* want, int N,
+                         int32_t* block_table, int64_t table_row_stride, int max_pages,
+                         int32_t* free_pages, const int32_t* free_count, int num_pages,
+                         int page_size, int64_t token_capacity, int32_t* new_lens,
+                         int32_t* cu_new, int32_t* slot_map, int32_t* positions,
+                         int32_t* new_count, int32_t* info, cudaStream_t stream);
+
+/*
+ * gdn_rope_inv_freq -- the rotary frequencies gdn_qk_norm_rope takes, made once
+ * per model: out[i] = base^(-2i / rope_dims), i < rope_dims / 2, in fp64,
+ * stretched for a context `factor` times longer than the trained one:
+ *   context == 0  all divided by factor (1 leaves them);
+ *   context > 0   by parts: with r_i = context * f_i / 2 pi (turns over the
+ *                 original context) and keep = clamp((r_i - beta_slow) /
+ *                 (beta_fast - beta_slow), 0, 1), f_i * (keep + (1 - keep) /
+ *                 factor).
+ * rope_dims is even and at most 256; base > 1; factor >= 1; beta_fast >
+ * beta_slow where context > 0.
+ */
+gdn_status gdn_rope_inv_freq(int rope_dims, double base, double factor, double context,
+                             double beta_fast, double beta_slow, double* out,
+                             cudaStream_t stream);
+
+/*
+ * gdn_qk_norm_rope -- per token: RMS-norm of each query and key head with its
+ * weight, rotary, and the append of the key and value rows to the paged cache,
+ * in one pass.
+ *   q [T, H_q, D], k, v [T, H_kv, D] x_dtype (any of the three types), row
+ *   strides per token. q NULL: keys and values only (q_out is not used); k and
+ *   v NULL: queries only (the caches are not used).
+ *   q_norm_w, k_norm_w  [D] w_dtype, or NULL: that side is not normed.
+ *   positions  [axes, T] int32, axes 1 or 3: pair i takes axis i mod axes.
+ *   inv_freq   [rope_dims / 2] fp64 (gdn_rope_inv_freq, or the caller's own),
+ *              8-byte aligned. rope_dims even, at most D; 0: no rotary, both
+ *              may be NULL.
+ *   interleaved  0: pair i is dims (i, i + rope_dims / 2); else (2i, 2i + 1).
+ *   rope_scale multiplies the turned dims (1 for plain rotary).
+ *   slot_map   [T] int32: token t's cache slot; a slot outside the cache
+ *              (without caches: a negative one) marks padding: none of the
+ *              token's rows is read or written. NULL: token t has slot t.
+ *              Slots of different tokens must differ.
+ *   q_out      [T, H_q, D] contiguous, out_dtype; may be q itself where q is
+ *              contiguous and of that type.
+ *   k_cache, v_cache  out_dtype (GDN_BF16 or GDN_F16) with their strides.
+ * Sums and rotations are in fp32 (angles exact to 2^-31 turns at any int32
+ * position), each value is rounded once; finite values past fp16's range become
+ * +-65504.
+ * A prompt's rows that gdn_attention_prefill returned go into the cache by a
+ * call without q, norm weights and rotary.
+ */
+gdn_status gdn_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k,
+                            int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                            gdn_dtype x_dtype, const void* q_norm_w, const void* k_norm_w,
+                            gdn_dtype w_dtype, float eps, const int32_t* positions, int axes,
+                            const double* inv_freq, int rope_dims, int interleaved,
+                            float rope_scale, const int32_t* slot_map, int64_t T, int H_q,
+                            int H_kv, int head_dim, void* q_out, void* k_cache,
+                            int64_t k_page_stride, int64_t k_token_stride,
+                            int64_t k_head_stride, void* v_cache, int64_t v_page_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, int num_pages,
+                            int page_size, gdn_dtype out_dtype, cudaStream_t stream);
+
+/*
+ * gdn_paged_attention_decode -- attention of one query token per sequence over
+ * its kv_lens[n] cached tokens:
+ *   o_h = sum_j softmax_j(scale * q_h . k_j) v_j,  j < kv_lens[n],
+ * query head h reading key-value head h / (H_q / H_kv).
+ *   q          [N, H_q, D] kv_dtype (GDN_F16 or GDN_BF16), row stride.
+ *   caches     kv_dtype with their strides.
+ *   block_table [N, max_pages] int32, row stride table_row_stride; entries past
+ *              a sequence's last page are not read.
+ *   gate       [N, H_q, D] bf16 (row stride) or NULL: o_h * sigmoid(gate_h).
+ *   o          [N, H_q, D] contiguous, any of the three types.
+ *   lse        [N, H_q] fp32 or NULL: log sum_j exp(scale * q_h . k_j), to join
+ *              outputs over parts of a context (the gate not included).
+ *   workspace  gdn_paged_attention_decode_workspace(H_q, H_kv, D) bytes, 16-byte
+ *              aligned; nothing has to be set before or kept after a call, but
+ *              calls whose executions overlap need their own.
+ * A sequence of length 0 gives a zero row (lse -inf). A length outside [0,
+ * max_pages * page_size] or a page outside [0, num_pages) gives NaN there and
+ * GDN_ERR_INVALID_ARG from gdn_attention_status(workspace); a bounded wait that
+ * ran out gives GDN_ERR_TIMEOUT there. H_q / H_kv is at most 16, N at most
+ * 65535. Cached rows behind a sequence's end are never used, whatever they
+ * hold. The result does not depend on which CTA runs first: equal calls give
+ * equal bits.
+ */
+size_t gdn_paged_attention_decode_workspace(int H_q, int H_kv, int head_dim);
+gdn_status gdn_paged_attention_decode(const void* q, int64_t q_row_stride, const void* k_cache,
+                                      int64_t k_page_stride, int64_t k_token_stride,
+                                      int64_t k_head_stride, const void* v_cache,
+                                      int64_t v_page_stride, int64_t v_token_stride,
+                                      int64_t v_head_stride, gdn_dtype kv_dtype, int num_pages,
+                                      int page_size, const int32_t* block_table,
+                                      int64_t table_row_stride, int max_pages,
+                                      const int32_t* kv_lens, const void* gate,
+                                      int64_t gate_row_stride, int N, int H_q, int H_kv,
+                                      int head_dim, float scale, void* o, gdn_dtype o_dtype,
+                                      float* lse, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
 
 #ifdef __cplusplus
 }
