@@ -10,10 +10,13 @@
 // one long sequence spreads over all SMs, and ragged lengths leave none idle;
 // the host needs no lengths (every CTA sums kv_lens itself).
 //
-// In a CTA one warp copies: it looks up each row's page and has the row copied
-// to shared memory (bulk copies of D * 2 bytes to rows padded by 16 bytes, so
-// ldmatrix meets no bank conflict), kStages blocks ahead and across sequence
-// ends. Four warps compute, 16 tokens of the block each, on mma.sync m16n8k16:
+// In a CTA two warps copy, one the K and one the V rows: they look up each
+// row's page and have it copied to shared memory (16-byte cp.async to rows padded
+// by 16 bytes, so ldmatrix meets no bank conflict), kStages blocks ahead and
+// across sequence ends. Row-sized bulk copies (cp.async.bulk of 2 D bytes) need
+// fewer instructions but the lanes of a warp issue them one after the other,
+// ~70 cycles each: 2.07 ms against XXX ms for 256 sequences of 4097
+// tokens. Four warps compute, 16 tokens of the block each, on mma.sync m16n8k16:
 //   S^T = K Q^T   (16 tokens x 8 heads), then
 //   O^T += V^T P^T (D x 8 heads), P^T turned in registers by movmatrix.
 // Tokens or head dims fill the 16 rows and the group's heads the 8 columns, so
@@ -38,7 +41,8 @@ using namespace sm100;
 
 constexpr int kTok = 64;                    // tokens per block
 constexpr int kCWarps = 4;                  // computing warps, 16 tokens each
-constexpr int kThreads = 32 * (kCWarps + 1);
+constexpr int kPWarps = 2;                  // copying warps: K, V
+constexpr int kThreads = 32 * (kCWarps + kPWarps);
 constexpr int kMaxCtas = 512;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
@@ -52,6 +56,7 @@ struct Cfg {
   static constexpr int kCtasPerSm = D == 256 ? 1 : (D == 128 ? 2 : 3);
   static constexpr int kStages = D == 128 && NT == 2 ? 2 : 3;
   static constexpr int kSmem = kStages * kStage;
+  static constexpr int kBatch = D == 256 && NT == 2 ? 2 : 4;   // fragments loaded ahead
   static constexpr int kPad = D + 4;                  // floats per head when pieces meet
   static_assert(kCWarps * kHeads * kPad * 4 <= kQ, "pieces meet in a block's K and V rows");
 };
@@ -76,6 +81,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 16 bytes to shared memory; zeros instead (and no read) with real = false
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real = true) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+// arrives on the barrier once this thread's copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -99,7 +115,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <>
 __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4],
                                                  uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -108,7 +124,7 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
 template <>
 __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4],
                                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -167,6 +183,14 @@ __device__ __forceinline__ void put_out(const PagedDecodeArgs& a, int64_t row, i
   }
 }
 
+template <int B>
+__device__ __forceinline__ float total(const float (&s)[B][4], int e) {
+  float v = s[0][e];
+#pragma unroll
+  for (int i = 1; i < B; ++i) v += s[i][e];
+  return v;
+}
+
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D, int NT, class Th>
@@ -177,7 +201,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   __shared__ uint64_t full[C::kStages], empty[C::kStages], meet;
   __shared__ BlockDesc desc[C::kStages];
   __shared__ float2 piece_ml[kCWarps][C::kHeads];
-  __shared__ int64_t warp_sum[kCWarps + 1];
+  __shared__ int64_t warp_sum[kCWarps + kPWarps];
   __shared__ int start_n, start_g, start_blk, trouble;
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -185,7 +209,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 32 * kPWarps + 1);
       mbar_init(&empty[i], kCWarps);
     }
     mbar_init(&meet, 32 * kCWarps);
@@ -207,7 +231,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   __syncthreads();
   int64_t before = incl - sum, U = 0;
 #pragma unroll
-  for (int w = 0; w <= kCWarps; ++w) {
+  for (int w = 0; w < kCWarps + kPWarps; ++w) {
     if (w < warp) before += warp_sum[w];
     U += warp_sum[w];
   }
@@ -230,79 +254,69 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   }
   __syncthreads();
 
-  if (warp == kCWarps) {
+  if (warp >= kCWarps) {
     // ------------------------------------------------------------- copies --
-    int64_t u = r0;
-    int n = start_n, g = start_g, blk = start_blk;
-    if (lane == 0) p.join[c] = make_int4(0, 0, 0, 0);
+    // One warp copies the K rows (and the queries), one the V rows; a row of D
+    // values takes D / 8 lanes.
+    constexpr int LPR = D / 8, RPI = 32 / LPR;
+    const bool is_v = warp != kCWarps;
+    const Th* cache = static_cast<const Th*>(is_v ? a.v_cache : a.k_cache);
+    const PageStrides cs = is_v ? a.vs : a.ks;
+    const uint32_t dst0 = smem_u32(sm) + (is_v ? C::kV : 0) + (lane / LPR) * C::kRow +
+                          (lane % LPR) * 16;
+    if (tid == 32 * kCWarps) p.join[c] = make_int4(0, 0, 0, 0);
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
-    int len = r1 > r0 ? (int)min((int64_t)max(a.kv_lens[n], 0), cap) : 0;
-    int nb = (int)(((int64_t)len + kTok - 1) / kTok);
+    // the unit whose rows are looked up: one ahead of the unit being copied, so
+    // that the table's latency passes behind the copies
+    int n = start_n, g = start_g, blk = start_blk, len = 0, nb = 0;
+    auto measure = [&] {
+      len = (int)min((int64_t)max(a.kv_lens[n], 0), cap);
+      nb = (int)(((int64_t)len + kTok - 1) / kTok);
+    };
+    int page[2], in_page[2];
+    auto lookup = [&] {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = blk * kTok + lane + 32 * e;
+        page[e] = -2;                              // no such row
+        if (t < len) {
+          const int j = t / a.page_size;
+          in_page[e] = t - j * a.page_size;
+          page[e] = a.table[(int64_t)n * a.table_row_stride + j];
+          if (page[e] < 0 || page[e] >= a.num_pages) page[e] = -1;
+        }
+      }
+    };
+    if (r1 > r0) {
+      measure();
+      lookup();
+    }
     bool first = true, bad = false, begins = blk == 0;
     int it = 0;
-    for (; u < r1; ++it) {
+    for (int64_t u = r0; u < r1; ++it) {
       const int st = it % C::kStages;
-      uint8_t* base = sm + st * C::kStage;
-      const int t0 = blk * kTok, ntok = min(kTok, len - t0);
-      int64_t koff[2], voff[2];
-      bool ok[2];
+      int64_t off[2];
+      bool wrong = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = lane + 32 * e;
-        ok[e] = false;
-        if (r < ntok) {
-          const int t = t0 + r, j = t / a.page_size, off = t - j * a.page_size;
-          const int page = a.table[(int64_t)n * a.table_row_stride + j];
-          ok[e] = page >= 0 && page < a.num_pages;
-          bad |= !ok[e];
-          koff[e] = page * a.ks.page + off * a.ks.token + g * a.ks.head;
-          voff[e] = page * a.vs.page + off * a.vs.token + g * a.vs.head;
-        }
+        off[e] = page[e] < 0 ? -1 : page[e] * cs.page + in_page[e] * cs.token + g * cs.head;
+        wrong |= page[e] == -1;
       }
-      const uint32_t rows = __popc(__ballot_sync(0xffffffffu, ok[0])) +
-                            __popc(__ballot_sync(0xffffffffu, ok[1]));
-      bad = __any_sync(0xffffffffu, bad);
+      bad |= __any_sync(0xffffffffu, wrong);
       const bool last_blk = blk + 1 == nb, last = last_blk || u + 1 == r1;
-      if (!mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs)) break;
-      if (lane == 0) {
-        BlockDesc b;
-        b.n = n;
-        b.g = g;
-        b.ntok = ntok;
-        b.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (bad ? kBad : 0);
-        // whole in this CTA: straight to the output; the piece that a CTA
-        // continues goes to slot 0, the one that it starts to slot 1
-        b.piece = begins ? (last_blk ? -1 : 1) : 0;
-        desc[st] = b;
-        if (bad) atomicMax(&trouble, 2);
-        mbar_arrive_expect_tx(&full[st], rows * 2 * (2 * D) + (first ? p.G * 2 * D : 0));
-        if (last && begins && !last_blk) {
-          const int64_t end = u + (nb - blk);           // unit behind this sequence piece
-          p.join[c] = make_int4(n, g, (int)((end * nc - 1) / U), 1);
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (ok[e]) {
-          const int r = lane + 32 * e;
-          bulk_g2s(base + r * C::kRow, static_cast<const Th*>(a.k_cache) + koff[e], 2 * D,
-                   &full[st]);
-          bulk_g2s(base + C::kV + r * C::kRow, static_cast<const Th*>(a.v_cache) + voff[e], 2 * D,
-                   &full[st]);
-        }
-      }
-      if (first && lane < p.G)
-        bulk_g2s(base + C::kQ + lane * C::kRow,
-                 static_cast<const Th*>(a.q) + n * a.q_row_stride +
-                     ((int64_t)g * p.G + lane) * D, 2 * D, &full[st]);
-      // next unit
+      BlockDesc b;
+      b.n = n;
+      b.g = g;
+      b.ntok = min(kTok, len - blk * kTok);
+      b.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (bad ? kBad : 0);
+      // whole in this CTA: straight to the output; the piece that a CTA
+      // continues goes to slot 0, the one that it starts to slot 1
+      b.piece = begins ? (last_blk ? -1 : 1) : 0;
+      const int64_t end = u + (nb - blk);          // unit behind this sequence and head
+      // on to the next unit
       ++u;
-      first = last;
-      if (last) bad = false;
-      if (!last_blk) {
-        ++blk;
-      } else {
+      ++blk;
+      if (last_blk) {
         blk = 0;
         begins = true;
         if (++g == a.Hkv && u < r1) {
@@ -313,23 +327,59 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             any = __ballot_sync(0xffffffffu, m < a.N && blocks_of(a, m) > 0);
             n += any ? __ffs(any) : 32;
           }
-          if (!any) { ++it; break; }               // only if lengths change during the call
-          len = (int)min((int64_t)max(a.kv_lens[n], 0), cap);
-          nb = (int)(((int64_t)len + kTok - 1) / kTok);
+          if (!any) u = r1;                        // only if lengths change during the call
+          else measure();
         }
       }
+      if (u < r1) lookup();
+      if (!mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs)) break;
+      const uint32_t dst = dst0 + st * C::kStage;
+      // no branch per row, and the shuffles of eight rows ahead of their copies:
+      // a lane's turn at a row then costs its instructions, not their latencies
+      constexpr int RB = 8;
+#pragma unroll
+      for (int r0 = 0; r0 < kTok; r0 += RB * RPI) {
+        int64_t o[RB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          const int r = r0 + i * RPI;
+          o[i] = __shfl_sync(0xffffffffu, off[r / 32], r % 32 + lane / LPR);
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          cp_async16(dst + (r0 + i * RPI) * C::kRow,
+                     cache + max(o[i], (int64_t)0) + (lane % LPR) * 8, o[i] >= 0);
+      }
+      if (!is_v) {
+        if (first) {
+          const Th* q = static_cast<const Th*>(a.q) + b.n * a.q_row_stride + (int64_t)b.g * p.G * D;
+          for (int i = lane; i < p.G * LPR; i += 32)
+            cp_async16(smem_u32(sm) + st * C::kStage + C::kQ + (i / LPR) * C::kRow +
+                       (i % LPR) * 16, q + i * 8);
+        }
+        if (lane == 0) {
+          desc[st] = b;
+          if (bad) atomicMax(&trouble, 2);
+          if (last && b.piece == 1)
+            p.join[c] = make_int4(b.n, b.g, (int)((end * nc - 1) / U), 1);
+          mbar_arrive(&full[st]);
+        }
+      }
+      cp_async_arrive(&full[st]);
+      first = last;
+      if (last) bad = false;
     }
-    // end mark, then wait for the copies in flight (a stage that is free again
-    // has had its copies)
+    // end mark, then wait for the copies in flight
     const int st = it % C::kStages;
-    bool fine = mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs);
-    if (fine && lane == 0) {
-      desc[st].flags = kEnd;
+    const bool fine = mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs);
+    if (fine) {
+      if (tid == 32 * kCWarps) {
+        desc[st].flags = kEnd;
+        mbar_arrive(&full[st]);
+      }
       mbar_arrive(&full[st]);
     }
-    const int i0 = fine ? it - C::kStages + 1 : it - C::kStages;
-    for (int i = max(0, i0); i < it; ++i)
-      fine &= mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kLimitNs);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!fine && lane == 0) atomicMax(&trouble, 3);
   } else {
     // ------------------------------------------------------------ compute --
@@ -387,17 +437,30 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       }
       const int nt = b.ntok - warp * 16;       // this warp's tokens
       if (nt > 0) {
-        float s[NT][2][4];
+        // fragments are loaded a batch ahead of the products that use them
+        constexpr int B = C::kBatch, KB = D / 16 / B;
+        float s[NT][B][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][0][e] = s[t][1][e] = 0.f;
+          for (int e = 0; e < B; ++e) s[t][e][0] = s[t][e][1] = s[t][e][2] = s[t][e][3] = 0.f;
+        uint32_t fr[2][B][4];
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t r[4];
-          ldsm4(base + k_off + kk * 32, r);
+        for (int i = 0; i < B; ++i) ldsm4(base + k_off + i * 32, fr[0][i]);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816<Th>(s[t][kk & 1], r, qf[t][kk][0], qf[t][kk][1]);
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            if (kb + 1 < KB)
+              ldsm4(base + k_off + ((kb + 1) * B + i) * 32, fr[(kb + 1) & 1][i]);
+            else                                   // the first V fragments, for after the softmax
+              ldsm4_t(base + C::kV + v_off + i * 32, fr[KB & 1][i]);
+          }
+#pragma unroll
+          for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              mma16816<Th>(s[t][i], fr[kb & 1][i], qf[t][kb * B + i][0], qf[t][kb * B + i][1]);
         }
         // scores of tokens row, row + 8 and heads 2 qd, 2 qd + 1
         const bool in0 = row < nt, in1 = row + 8 < nt;
@@ -408,7 +471,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[e] = (e < 2 ? in0 : in1) ? (s[t][0][e] + s[t][1][e]) * p.sl2 : -INFINITY;
+            x[e] = (e < 2 ? in0 : in1) ? total(s[t], e) * p.sl2 : -INFINITY;
           const bool rise = (h0 < p.G && fmaxf(x[0], x[2]) > m[t][0] + 8.f) ||
                             (h0 + 1 < p.G && fmaxf(x[1], x[3]) > m[t][1] + 8.f);
           if (__any_sync(0xffffffffu, rise)) {
@@ -444,23 +507,22 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             lo[t][e] = transpose8x8(lo[t][e]);
           }
         }
-        // rows behind the last token were not copied: what is there must not
-        // meet a weight of 0
-        const uint32_t keep0 = (2 * qd < nt ? 0xffffu : 0u) | (2 * qd + 1 < nt ? 0xffff0000u : 0u);
-        const uint32_t keep1 =
-            (2 * qd + 8 < nt ? 0xffffu : 0u) | (2 * qd + 9 < nt ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          uint32_t r[4];
-          ldsm4_t(base + C::kV + v_off + j * 32, r);
-          r[0] &= keep0;
-          r[1] &= keep0;
-          r[2] &= keep1;
-          r[3] &= keep1;
+        for (int vb = 0; vb < KB; ++vb) {
+          const uint32_t (&cur)[B][4] = fr[(KB + vb) & 1];
+          if (vb + 1 < KB) {
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+              ldsm4_t(base + C::kV + v_off + ((vb + 1) * B + i) * 32, fr[(KB + vb + 1) & 1][i]);
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma16816<Th>(o[t][j], r, hi[t][0], hi[t][1]);
-            mma16816<Th>(o[t][j], r, lo[t][0], lo[t][1]);
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+              mma16816<Th>(o[t][vb * B + i], cur[i], hi[t][0], hi[t][1]);
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+              mma16816<Th>(o[t][vb * B + i], cur[i], lo[t][0], lo[t][1]);
           }
         }
       }
@@ -524,7 +586,6 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             if (d == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, L);
           }
         }
-        fence_proxy_async_smem();     // plain accesses here, then the next copies
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
