@@ -41,8 +41,6 @@ using namespace sm100;
 
 constexpr int kTok = 64;                    // tokens per block
 constexpr int kCWarps = 4;                  // computing warps, 16 tokens each
-constexpr int kPWarps = 2;                  // copying warps: K, V
-constexpr int kThreads = 32 * (kCWarps + kPWarps);
 constexpr int kMaxCtas = 512;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
@@ -53,6 +51,8 @@ struct Cfg {
   static constexpr int kV = kTok * kRow;              // offsets within a stage
   static constexpr int kQ = 2 * kTok * kRow;
   static constexpr int kStage = kQ + kHeads * kRow;
+  static constexpr int kPWarps = D == 256 ? 4 : 2;    // copying warps, half for K, half for V
+  static constexpr int kThreads = 32 * (kCWarps + kPWarps);
   static constexpr int kCtasPerSm = D == 256 ? 1 : (D == 128 ? 2 : 3);
   static constexpr int kStages = D == 128 && NT == 2 ? 2 : 3;
   static constexpr int kSmem = kStages * kStage;
@@ -61,7 +61,7 @@ struct Cfg {
   static_assert(kCWarps * kHeads * kPad * 4 <= kQ, "pieces meet in a block's K and V rows");
 };
 
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kBad = 8 };
+enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
 
 struct BlockDesc { int n, g, ntok, flags, piece, pad[3]; };   // piece: -1 or 0 / 1
 
@@ -194,14 +194,15 @@ __device__ __forceinline__ float total(const float (&s)[B][4], int e) {
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D, int NT, class Th>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
 paged_split_kernel(const __grid_constant__ PagedParams p) {
   using C = Cfg<D, NT>;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], meet;
   __shared__ BlockDesc desc[C::kStages];
+  __shared__ int wrong_page[C::kStages][C::kPWarps];    // met by each copying warp
   __shared__ float2 piece_ml[kCWarps][C::kHeads];
-  __shared__ int64_t warp_sum[kCWarps + kPWarps];
+  __shared__ int64_t warp_sum[kCWarps + C::kPWarps];
   __shared__ int start_n, start_g, start_blk, trouble;
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -209,7 +210,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 32 * kPWarps + 1);
+      mbar_init(&full[i], 33 * C::kPWarps);
       mbar_init(&empty[i], kCWarps);
     }
     mbar_init(&meet, 32 * kCWarps);
@@ -217,7 +218,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     trouble = start_n = start_g = start_blk = 0;
   }
   // units before each thread's run of sequences
-  const int per = (a.N + kThreads - 1) / kThreads;
+  const int per = (a.N + C::kThreads - 1) / C::kThreads;
   const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
   int64_t sum = 0;
   for (int n = n0; n < n1; ++n) sum += blocks_of(a, n);
@@ -231,7 +232,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   __syncthreads();
   int64_t before = incl - sum, U = 0;
 #pragma unroll
-  for (int w = 0; w < kCWarps + kPWarps; ++w) {
+  for (int w = 0; w < kCWarps + C::kPWarps; ++w) {
     if (w < warp) before += warp_sum[w];
     U += warp_sum[w];
   }
@@ -256,14 +257,16 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 
   if (warp >= kCWarps) {
     // ------------------------------------------------------------- copies --
-    // One warp copies the K rows (and the queries), one the V rows; a row of D
-    // values takes D / 8 lanes.
+    // Even warps copy K rows, odd ones V rows, each an even share of the block;
+    // the first also the queries. A row of D values takes D / 8 lanes.
     constexpr int LPR = D / 8, RPI = 32 / LPR;
-    const bool is_v = warp != kCWarps;
+    constexpr int kRows = 2 * kTok / C::kPWarps, E = kRows / 32;
+    const bool is_v = (warp - kCWarps) & 1, lead = warp == kCWarps;
+    const int row0 = (warp - kCWarps) / 2 * kRows;
     const Th* cache = static_cast<const Th*>(is_v ? a.v_cache : a.k_cache);
     const PageStrides cs = is_v ? a.vs : a.ks;
-    const uint32_t dst0 = smem_u32(sm) + (is_v ? C::kV : 0) + (lane / LPR) * C::kRow +
-                          (lane % LPR) * 16;
+    const uint32_t dst0 = smem_u32(sm) + (is_v ? C::kV : 0) +
+                          (row0 + lane / LPR) * C::kRow + (lane % LPR) * 16;
     if (tid == 32 * kCWarps) p.join[c] = make_int4(0, 0, 0, 0);
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
     // the unit whose rows are looked up: one ahead of the unit being copied, so
@@ -273,11 +276,11 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       len = (int)min((int64_t)max(a.kv_lens[n], 0), cap);
       nb = (int)(((int64_t)len + kTok - 1) / kTok);
     };
-    int page[2], in_page[2];
+    int page[E], in_page[E];
     auto lookup = [&] {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = blk * kTok + lane + 32 * e;
+      for (int e = 0; e < E; ++e) {
+        const int t = blk * kTok + row0 + lane + 32 * e;
         page[e] = -2;                              // no such row
         if (t < len) {
           const int j = t / a.page_size;
@@ -295,20 +298,20 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     int it = 0;
     for (int64_t u = r0; u < r1; ++it) {
       const int st = it % C::kStages;
-      int64_t off[2];
+      int64_t off[E];
       bool wrong = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         off[e] = page[e] < 0 ? -1 : page[e] * cs.page + in_page[e] * cs.token + g * cs.head;
         wrong |= page[e] == -1;
       }
-      bad |= __any_sync(0xffffffffu, wrong);
+      bad |= __any_sync(0xffffffffu, wrong);       // a warp's own rows
       const bool last_blk = blk + 1 == nb, last = last_blk || u + 1 == r1;
       BlockDesc b;
       b.n = n;
       b.g = g;
       b.ntok = min(kTok, len - blk * kTok);
-      b.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (bad ? kBad : 0);
+      b.flags = (first ? kFirst : 0) | (last ? kLast : 0);
       // whole in this CTA: straight to the output; the piece that a CTA
       // continues goes to slot 0, the one that it starts to slot 1
       b.piece = begins ? (last_blk ? -1 : 1) : 0;
@@ -338,7 +341,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       // a lane's turn at a row then costs its instructions, not their latencies
       constexpr int RB = 8;
 #pragma unroll
-      for (int r0 = 0; r0 < kTok; r0 += RB * RPI) {
+      for (int r0 = 0; r0 < kRows; r0 += RB * RPI) {
         int64_t o[RB];
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
@@ -350,20 +353,21 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           cp_async16(dst + (r0 + i * RPI) * C::kRow,
                      cache + max(o[i], (int64_t)0) + (lane % LPR) * 8, o[i] >= 0);
       }
-      if (!is_v) {
-        if (first) {
-          const Th* q = static_cast<const Th*>(a.q) + b.n * a.q_row_stride + (int64_t)b.g * p.G * D;
-          for (int i = lane; i < p.G * LPR; i += 32)
-            cp_async16(smem_u32(sm) + st * C::kStage + C::kQ + (i / LPR) * C::kRow +
-                       (i % LPR) * 16, q + i * 8);
-        }
-        if (lane == 0) {
+      if (lead && first) {
+        const Th* q = static_cast<const Th*>(a.q) + b.n * a.q_row_stride + (int64_t)b.g * p.G * D;
+        for (int i = lane; i < p.G * LPR; i += 32)
+          cp_async16(smem_u32(sm) + st * C::kStage + C::kQ + (i / LPR) * C::kRow +
+                     (i % LPR) * 16, q + i * 8);
+      }
+      if (lane == 0) {
+        if (lead) {
           desc[st] = b;
-          if (bad) atomicMax(&trouble, 2);
           if (last && b.piece == 1)
             p.join[c] = make_int4(b.n, b.g, (int)((end * nc - 1) / U), 1);
-          mbar_arrive(&full[st]);
         }
+        wrong_page[st][warp - kCWarps] = bad;
+        if (bad) atomicMax(&trouble, 2);
+        mbar_arrive(&full[st]);
       }
       cp_async_arrive(&full[st]);
       first = last;
@@ -373,10 +377,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     const int st = it % C::kStages;
     const bool fine = mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs);
     if (fine) {
-      if (tid == 32 * kCWarps) {
-        desc[st].flags = kEnd;
-        mbar_arrive(&full[st]);
-      }
+      if (tid == 32 * kCWarps) desc[st].flags = kEnd;
+      if (lane == 0) mbar_arrive(&full[st]);
       mbar_arrive(&full[st]);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -554,6 +556,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         if (!mbar_wait_bounded(&meet, meets & 1, kLimitNs)) { dead = true; break; }
         ++meets;
         const float* all = reinterpret_cast<const float*>(stage);
+        int bad = 0;
+#pragma unroll
+        for (int w = 0; w < C::kPWarps; ++w) bad |= wrong_page[st][w];
         for (int i = tid; i < p.G * (D / 4); i += 32 * kCWarps) {
           const int h = i / (D / 4), d = 4 * (i % (D / 4));
           float M = -INFINITY;
@@ -572,7 +577,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             y[2] += f * v.z;
             y[3] += f * v.w;
           }
-          if (b.flags & kBad) L = __int_as_float(0x7fc00000);
+          if (bad) L = __int_as_float(0x7fc00000);
           const int hq = b.g * p.G + h;
           if (b.piece < 0) {
             const float inv = 1.f / L;
@@ -671,7 +676,7 @@ cudaError_t launch_split(const PagedParams& p, int sms) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   const int grid = min(sms * C::kCtasPerSm, kMaxCtas);
-  paged_split_kernel<D, NT, Th><<<grid, kThreads, C::kSmem, p.a.stream>>>(p);
+  paged_split_kernel<D, NT, Th><<<grid, C::kThreads, C::kSmem, p.a.stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join starts while the split's last CTAs end, and waits for them
