@@ -545,8 +545,20 @@ def gdn_attention_status(workspace, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ paged cache
+# These calls take a few microseconds on the GPU when a step is small, so their
+# checks touch each tensor once or twice and build no message unless one fails.
 _DTYPE3 = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float16: GDN_F16}
+_HALF = (torch.bfloat16, torch.float16)
 _HERE_NOW = contextlib.nullcontext()
+_fn = {}
+
+
+def _entry(name):
+    """A C entry point, looked up once."""
+    fn = _fn.get(name)
+    if fn is None:
+        fn = _fn[name] = getattr(load(), name)
+    return fn
 
 
 def _dtype3(t: torch.dtype, name) -> int:
@@ -556,62 +568,83 @@ def _dtype3(t: torch.dtype, name) -> int:
     return code
 
 
-def _one_device(*tensors):
-    """The CUDA device that all given tensors are on."""
+def _one_device(*tensors) -> int:
+    """The index of the CUDA device that all given tensors are on."""
     dev = None
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libgdn takes CUDA tensors only (no CPU path)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+        if t is not None:
+            d = t.get_device()               # -1 on the CPU
+            if d != dev:
+                if d < 0:
+                    raise ValueError("libgdn takes CUDA tensors only (no CPU path)")
+                if dev is not None:
+                    raise ValueError(f"tensors on cuda:{dev} and cuda:{d}: one device is needed")
+                dev = d
     return dev
 
 
 def _on(dev, stream):
-    """Makes `dev` and `stream` current for the allocations and the launch of a
-    call, so that buffers made for it belong to the stream that uses them."""
+    """Makes device `dev` and `stream` current for the allocations and the launch
+    of a call, so that buffers made for it belong to the stream that uses them."""
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.device_index != dev:
+            raise ValueError(f"stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         return torch.cuda.device(dev)
     return _HERE_NOW
 
 
-def _rows32(t, name, shape=None):
-    """Pointer and row stride of an int32 [N, M] tensor with dense rows."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape or '[N, max_pages]'}")
-    if t.dtype != torch.int32:
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(t, shape, name, dtype):
+    """A contiguous tensor of this shape and dtype (None: not given)."""
+    if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
+        _expect(t, shape, name, dtype)
+
+
+def _rows32(t, N, name):
+    """Row stride of an int32 [N, M] tensor with dense rows."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != N:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected ({N}, max_pages)")
+    if t.dtype is not torch.int32:
         raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]     # one row: no stride is used
+    return stride[0] if N > 1 else shape[1]               # one row: no stride is used
 
 
-def _cache_strides(t, name, shape=None, dtype=None):
+def _cache_strides(t, name, shape, dtype):
     """(page, token, head) strides of a [pages, page_size, H_kv, D] cache view."""
-    if t.dim() != 4 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
-                         f"{shape or '[num_pages, page_size, H_kv, D]'}")
-    if dtype is not None and t.dtype != dtype:
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    D = t.shape[3]
-    if t.stride(3) != 1:
-        raise ValueError(f"{name}: each row of {D} values must be contiguous")
-    # the stride of a dimension of one is never used
-    return [t.stride(i) if t.shape[i] > 1 else D for i in range(3)]
+    page, token, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: each row of {shape[3]} values must be contiguous")
+    if 1 in shape:                       # the stride of a dimension of one is never used
+        page, token, head = (n if size > 1 else shape[3]
+                             for n, size in zip((page, token, head), shape))
+    return page, token, head
 
 
-def _head_rows3(t, shape, name, dtype):
-    _expect(t, shape, name, dtype, contiguous=False)
-    stride = _row_stride(t)
-    return stride if t.shape[0] > 1 else shape[1] * shape[2]
+def _head_stride(t, shape, name, dtype):
+    """Row stride of [n, H, D] with dense heads."""
+    if t.shape != shape or t.dtype is not dtype:
+        _expect(t, shape, name, dtype, contiguous=False)
+    row, head, one = t.stride()
+    if one != 1 or (head != shape[2] and shape[1] != 1):
+        raise ValueError(f"{name}: trailing dimensions must be contiguous")
+    return row if shape[0] > 1 else shape[1] * shape[2]
 
 
 class PagePlan(NamedTuple):
@@ -622,9 +655,9 @@ class PagePlan(NamedTuple):
     new_lens: torch.Tensor
     cu_new: torch.Tensor
     slot_map: torch.Tensor
-    positions: Optional[torch.Tensor]
+    positions: torch.Tensor
     new_count: torch.Tensor
-    info: Optional[torch.Tensor]
+    info: torch.Tensor
 
 
 def gdn_page_plan(lens, want, block_table, free_pages, free_count, page_size, *,
@@ -639,34 +672,34 @@ def gdn_page_plan(lens, want, block_table, free_pages, free_count, page_size, *,
     they are: adopt new_lens and new_count to go on. Returns a PagePlan."""
     N, P = lens.numel(), free_pages.numel()
     if slot_map is not None:
-        if token_capacity not in (None, slot_map.numel()):
+        if token_capacity is not None and token_capacity != slot_map.numel():
             raise ValueError("token_capacity is not slot_map's length")
         token_capacity = slot_map.numel()
     if token_capacity is None:
         raise ValueError("give token_capacity or slot_map")
     i32 = torch.int32
-    _expect(lens, (N,), "lens", i32)
-    _expect(want, (N,), "want", i32)
-    row = _rows32(block_table, "block_table", (N, block_table.shape[-1]))
-    _expect(free_pages, (P,), "free_pages", i32)
-    _expect(free_count, (1,), "free_count", i32)
-    _expect(new_lens, (N,), "new_lens", i32)
-    _expect(cu_new, (N + 1,), "cu_new", i32)
-    _expect(slot_map, (token_capacity,), "slot_map", i32)
-    _expect(positions, (token_capacity,), "positions", i32)
-    _expect(new_count, (1,), "new_count", i32)
-    _expect(info, (4,), "info", i32)
+    _dense(lens, (N,), "lens", i32)
+    _dense(want, (N,), "want", i32)
+    row = _rows32(block_table, N, "block_table")
+    _dense(free_pages, (P,), "free_pages", i32)
+    _dense(free_count, (1,), "free_count", i32)
+    _dense(new_lens, (N,), "new_lens", i32)
+    _dense(cu_new, (N + 1,), "cu_new", i32)
+    _dense(slot_map, (token_capacity,), "slot_map", i32)
+    _dense(positions, (token_capacity,), "positions", i32)
+    _dense(new_count, (1,), "new_count", i32)
+    _dense(info, (4,), "info", i32)
     dev = _one_device(lens, want, block_table, free_pages, free_count, new_lens, cu_new, slot_map,
                       positions, new_count, info)
     with _on(dev, stream):
         def buf(t, n):
-            return torch.empty(n, dtype=i32, device=dev) if t is None else t
+            return torch.empty(n, dtype=i32, device=lens.device) if t is None else t
         out = PagePlan(buf(new_lens, N), buf(cu_new, N + 1), buf(slot_map, token_capacity),
                        buf(positions, token_capacity), buf(new_count, 1), buf(info, 4))
-        _check("gdn_page_plan", load().gdn_page_plan(
+        _check("gdn_page_plan", _entry("gdn_page_plan")(
             lens.data_ptr(), want.data_ptr(), N, block_table.data_ptr(), row,
             block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(), P, page_size,
-            token_capacity, *(t.data_ptr() for t in out), _stream(None, dev)))
+            token_capacity, *[t.data_ptr() for t in out], _raw_stream(dev)))
     return out
 
 
@@ -678,12 +711,12 @@ def gdn_rope_inv_freq(rope_dims, base=1e7, *, factor=1.0, context=0, beta_fast=3
     if out is None:
         out = torch.empty(rope_dims // 2, dtype=torch.float64,
                           device="cuda" if device is None else device)
-    _expect(out, (rope_dims // 2,), "out", torch.float64)
+    _dense(out, (rope_dims // 2,), "out", torch.float64)
     dev = _one_device(out)
     with _on(dev, stream):
-        _check("gdn_rope_inv_freq", load().gdn_rope_inv_freq(
+        _check("gdn_rope_inv_freq", _entry("gdn_rope_inv_freq")(
             rope_dims, base, factor, context, beta_fast, beta_slow, out.data_ptr(),
-            _stream(None, dev)))
+            _raw_stream(dev)))
     return out
 
 
@@ -702,60 +735,69 @@ def gdn_qk_norm_rope(q, k, v, k_cache=None, v_cache=None, *, slot_map=None, q_no
         raise ValueError("give q, or k and v with both caches, or all")
     if x.dim() != 3:
         raise ValueError(f"q, k, v: {x.dim()} dimensions, expected [T, H, D]")
-    T, D = x.shape[0], x.shape[2]
-    H_q = q.shape[1] if q is not None else 0
-    H_kv = k.shape[1] if k is not None else 0
-    P = page = ks = vs = 0
+    T, H_q, D = x.shape
+    dtype = x.dtype
+    H_kv = P = page = qs = ks = vs = 0
     k_str = v_str = (0, 0, 0)
+    if q is None:
+        H_q = 0
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        qs = _head_stride(q, (T, H_q, D), "q", dtype)
     if k is not None:
-        ks = _head_rows3(k, (T, H_kv, D), "k", x.dtype)
-        vs = _head_rows3(v, (T, H_kv, D), "v", x.dtype)
-        P, page = k_cache.shape[0], k_cache.shape[1]
-        k_str = _cache_strides(k_cache, "k_cache", (P, page, H_kv, D))
-        v_str = _cache_strides(v_cache, "v_cache", (P, page, H_kv, D), k_cache.dtype)
-        if out_dtype not in (None, k_cache.dtype):
+        H_kv = k.shape[1]
+        shape = (T, H_kv, D)
+        ks = _head_stride(k, shape, "k", dtype)
+        vs = _head_stride(v, shape, "v", dtype)
+        P, page = k_cache.shape[:2]
+        shape = (P, page, H_kv, D)
+        k_str = _cache_strides(k_cache, "k_cache", shape, k_cache.dtype)
+        v_str = _cache_strides(v_cache, "v_cache", shape, k_cache.dtype)
+        if out_dtype is not None and out_dtype is not k_cache.dtype:
             raise ValueError(f"out_dtype {out_dtype}: q_out has the caches' dtype")
         out_dtype = k_cache.dtype
     elif out_dtype is None:
         out_dtype = q_out.dtype if q_out is not None else torch.float16
-    if out_dtype not in (torch.bfloat16, torch.float16):
+    if out_dtype not in _HALF:
         raise ValueError(f"caches and q_out are bf16 or fp16, got {out_dtype}")
-    qs = _head_rows3(q, (T, H_q, D), "q", x.dtype) if q is not None else 0
-    if q is None and q_out is not None:
-        raise ValueError("q_out without q")
-    _expect(q_out, (T, H_q, D), "q_out", out_dtype)
+    _dense(q_out, (T, H_q, D), "q_out", out_dtype)
     w = q_norm_w if q_norm_w is not None else k_norm_w
-    _expect(q_norm_w, (D,), "q_norm_w", None)
-    _expect(k_norm_w, (D,), "k_norm_w", None if w is None else w.dtype)
-    _expect(slot_map, (T,), "slot_map", torch.int32)
+    if w is not None:
+        _dense(q_norm_w, (D,), "q_norm_w", w.dtype)
+        _dense(k_norm_w, (D,), "k_norm_w", w.dtype)
+    _dense(slot_map, (T,), "slot_map", torch.int32)
     R, axes = 0, 1
     if inv_freq is not None:
-        R = 2 * inv_freq.numel()
-        _expect(inv_freq, (R // 2,), "inv_freq", torch.float64)
         if positions is None:
             raise ValueError("rotary needs positions")
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        _expect(positions, (T,) if positions.dim() == 1 else (3, T), "positions", torch.int32)
+        R = 2 * inv_freq.numel()
+        _dense(inv_freq, (R // 2,), "inv_freq", torch.float64)
+        if positions.dim() == 1:
+            _dense(positions, (T,), "positions", torch.int32)
+        else:
+            axes = 3
+            _dense(positions, (3, T), "positions", torch.int32)
     elif positions is not None:
         raise ValueError("positions without inv_freq")
-    dev = _one_device(q, k, v, k_cache, v_cache, slot_map, q_norm_w, k_norm_w, positions,
+    dev = _one_device(x, k, v, k_cache, v_cache, slot_map, q_norm_w, k_norm_w, positions,
                       inv_freq, q_out)
-    xd = _dtype3(x.dtype, "q, k, v")
+    xd = _dtype3(dtype, "q, k, v")
     wd = GDN_F32 if w is None else _dtype3(w.dtype, "norm weights")
     with _on(dev, stream):
         if q is not None and q_out is None:
-            q_out = torch.empty((T, H_q, D), dtype=out_dtype, device=dev)
-        _check("gdn_qk_norm_rope", load().gdn_qk_norm_rope(
-            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, xd, _ptr(q_norm_w), _ptr(k_norm_w), wd, eps,
-            _ptr(positions), axes, _ptr(inv_freq), R, int(bool(interleaved)), rope_scale,
-            _ptr(slot_map), T, H_q, H_kv, D, _ptr(q_out), _ptr(k_cache), *k_str, _ptr(v_cache),
-            *v_str, P, page, _DTYPE3[out_dtype], _stream(None, dev)))
+            q_out = torch.empty((T, H_q, D), dtype=out_dtype, device=q.device)
+        _check("gdn_qk_norm_rope", _entry("gdn_qk_norm_rope")(
+            _addr(q), qs, _addr(k), ks, _addr(v), vs, xd, _addr(q_norm_w), _addr(k_norm_w), wd,
+            eps, _addr(positions), axes, _addr(inv_freq), R, 1 if interleaved else 0, rope_scale,
+            _addr(slot_map), T, H_q, H_kv, D, _addr(q_out), _addr(k_cache), *k_str,
+            _addr(v_cache), *v_str, P, page, _DTYPE3[out_dtype], _raw_stream(dev)))
     return q_out
 
 
 def gdn_paged_attention_decode_workspace(H_q, H_kv, head_dim=ATTN_HEAD_DIM) -> int:
     """Bytes of workspace gdn_paged_attention_decode needs (any N, any lengths)."""
-    return int(load().gdn_paged_attention_decode_workspace(H_q, H_kv, head_dim))
+    return _entry("gdn_paged_attention_decode_workspace")(H_q, H_kv, head_dim)
 
 
 def gdn_paged_attention_decode(q, k_cache, v_cache, block_table, kv_lens, *, gate=None,
@@ -767,40 +809,43 @@ def gdn_paged_attention_decode(q, k_cache, v_cache, block_table, kv_lens, *, gat
     max_pages] (int32). gate [N, H_q, D] bf16: times sigmoid(gate). lse [N, H_q]
     fp32 receives the log of the softmax sums. Returns o [N, H_q, D] (o_dtype,
     bf16 unless given). A sequence of length 0 gives zeros."""
-    if q.dim() != 3:
-        raise ValueError(f"q: {q.dim()} dimensions, expected [N, H_q, D]")
-    N, H_q, D = q.shape
-    k_str = _cache_strides(k_cache, "k_cache")
-    P, page, H_kv, _ = k_cache.shape
-    if k_cache.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"caches are bf16 or fp16, got {k_cache.dtype}")
-    v_str = _cache_strides(v_cache, "v_cache", (P, page, H_kv, D), k_cache.dtype)
-    if k_cache.shape[3] != D:
-        raise ValueError(f"k_cache: head dim {k_cache.shape[3]}, q has {D}")
-    qs = _head_rows3(q, (N, H_q, D), "q", k_cache.dtype)
-    row = _rows32(block_table, "block_table", (N, block_table.shape[-1]))
-    _expect(kv_lens, (N,), "kv_lens", torch.int32)
-    gs = 0
-    if gate is not None:
-        gs = _head_rows3(gate, (N, H_q, D), "gate", torch.bfloat16)
-    _expect(o, (N, H_q, D), "o")
-    _expect(lse, (N, H_q), "lse", torch.float32)
-    if o is None:
-        o_dtype = o_dtype or torch.bfloat16
-    elif o_dtype not in (None, o.dtype):
-        raise ValueError(f"o: dtype {o.dtype}, expected {o_dtype}")
-    od = _dtype3(o_dtype if o is None else o.dtype, "o")
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError(f"q: {q.dim()} dimensions, expected [N, H_q, D]; k_cache: "
+                         f"{k_cache.dim()}, expected [num_pages, page_size, H_kv, D]")
+    q_shape, shape, dtype = q.shape, k_cache.shape, k_cache.dtype
+    N, H_q, D = q_shape
+    P, page, H_kv, Dk = shape
+    if dtype not in _HALF:
+        raise ValueError(f"caches are bf16 or fp16, got {dtype}")
+    if Dk != D:
+        raise ValueError(f"k_cache: head dim {Dk}, q has {D}")
+    k_str = _cache_strides(k_cache, "k_cache", shape, dtype)
+    v_str = _cache_strides(v_cache, "v_cache", shape, dtype)
+    qs = _head_stride(q, q_shape, "q", dtype)
+    row = _rows32(block_table, N, "block_table")
+    _dense(kv_lens, (N,), "kv_lens", torch.int32)
+    gs = _head_stride(gate, q_shape, "gate", torch.bfloat16) if gate is not None else 0
+    if o is not None:
+        if o_dtype is not None and o_dtype is not o.dtype:
+            raise ValueError(f"o: dtype {o.dtype}, expected {o_dtype}")
+        o_dtype = o.dtype
+        _dense(o, q_shape, "o", o_dtype)
+    elif o_dtype is None:
+        o_dtype = torch.bfloat16
+    od = _dtype3(o_dtype, "o")
+    _dense(lse, (N, H_q), "lse", torch.float32)
     dev = _one_device(q, k_cache, v_cache, block_table, kv_lens, gate, o, lse, workspace)
     with _on(dev, stream):
         if o is None:
-            o = torch.empty((N, H_q, D), dtype=o_dtype, device=dev)
+            o = torch.empty(q_shape, dtype=o_dtype, device=q.device)
         if workspace is None:
             workspace = torch.empty(
                 max(gdn_paged_attention_decode_workspace(H_q, H_kv, D), 256),
-                dtype=torch.uint8, device=dev)
-        _check("gdn_paged_attention_decode", load().gdn_paged_attention_decode(
-            _ptr(q), qs, _ptr(k_cache), *k_str, _ptr(v_cache), *v_str, _DTYPE3[k_cache.dtype],
-            P, page, _ptr(block_table), row, block_table.shape[1], _ptr(kv_lens), _ptr(gate), gs,
-            N, H_q, H_kv, D, D ** -0.5 if scale is None else scale, _ptr(o), od, _ptr(lse),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(None, dev)))
+                dtype=torch.uint8, device=q.device)
+        _check("gdn_paged_attention_decode", _entry("gdn_paged_attention_decode")(
+            q.data_ptr(), qs, k_cache.data_ptr(), *k_str, v_cache.data_ptr(), *v_str,
+            _DTYPE3[dtype], P, page, block_table.data_ptr(), row, block_table.shape[1],
+            kv_lens.data_ptr(), _addr(gate), gs, N, H_q, H_kv, D,
+            D ** -0.5 if scale is None else scale, o.data_ptr(), od, _addr(lse),
+            workspace.data_ptr(), workspace.nbytes, _raw_stream(dev)))
     return o

@@ -4,7 +4,7 @@
 //
 // The K and V rows cross HBM once, so bytes bound it (2 * G FLOP per cached
 // byte for a group of G query heads, a few percent of the tensor rate). The work
-// is cut evenly: the units are (sequence, key-value head, 64-token block) in
+// is cut evenly: the units are (sequence, key-value head, block of 64 or 128 tokens) in
 // that order, the grid is as many CTAs as fit on the chip at once, and CTA c
 // takes units [c U / C, (c + 1) U / C) whatever sequences they belong to. So
 // one long sequence spreads over all SMs, and ragged lengths leave none idle;
@@ -39,22 +39,23 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTok = 64;                    // tokens per block
-constexpr int kCWarps = 4;                  // computing warps, 16 tokens each
+constexpr int kCWarps = 4;                  // computing warps
 constexpr int kMaxCtas = 512;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 template <int D, int NT>
 struct Cfg {
+  static constexpr int kTiles = D == 256 ? 1 : 2;     // 16-token tiles per warp and block
+  static constexpr int kTok = 16 * kTiles * kCWarps;  // tokens per block
   static constexpr int kHeads = 8 * NT;               // head columns
   static constexpr int kRow = 2 * D + 16;             // bytes per shared-memory row
   static constexpr int kV = kTok * kRow;              // offsets within a stage
   static constexpr int kQ = 2 * kTok * kRow;
   static constexpr int kStage = kQ + kHeads * kRow;
-  static constexpr int kPWarps = D == 256 ? 4 : 2;    // copying warps, half for K, half for V
+  static constexpr int kPWarps = 4;                   // copying warps, half for K, half for V
   static constexpr int kThreads = 32 * (kCWarps + kPWarps);
-  static constexpr int kCtasPerSm = D == 256 ? 1 : (D == 128 ? 2 : 3);
-  static constexpr int kStages = D == 128 && NT == 2 ? 2 : 3;
+  static constexpr int kCtasPerSm = D == 64 && NT == 1 ? 2 : 1;
+  static constexpr int kStages = D == 64 && NT == 2 ? 5 : 3;
   static constexpr int kSmem = kStages * kStage;
   static constexpr int kBatch = D == 256 && NT == 2 ? 2 : 4;   // fragments loaded ahead
   static constexpr int kPad = D + 4;                  // floats per head when pieces meet
@@ -150,9 +151,10 @@ __device__ __forceinline__ void split2(float a, float b, __nv_bfloat16, uint32_t
 __device__ __forceinline__ bool len_ok(const PagedDecodeArgs& a, int len) {
   return len >= 0 && (int64_t)len <= (int64_t)a.max_pages * a.page_size;
 }
-__device__ __forceinline__ int blocks_of(const PagedDecodeArgs& a, int n) {
-  const int len = a.kv_lens[n];
-  return len_ok(a, len) ? (int)(((int64_t)len + kTok - 1) / kTok) : 0;
+// blocks of TOK tokens; a length out of range has none
+template <int TOK>
+__device__ __forceinline__ int blocks_of(const PagedDecodeArgs& a, int len) {
+  return len_ok(a, len) ? (int)(((int64_t)len + TOK - 1) / TOK) : 0;
 }
 
 // four output values of one (sequence, head): gate and round
@@ -197,13 +199,14 @@ template <int D, int NT, class Th>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
 paged_split_kernel(const __grid_constant__ PagedParams p) {
   using C = Cfg<D, NT>;
+  constexpr int kTok = C::kTok;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], meet;
   __shared__ BlockDesc desc[C::kStages];
   __shared__ int wrong_page[C::kStages][C::kPWarps];    // met by each copying warp
   __shared__ float2 piece_ml[kCWarps][C::kHeads];
   __shared__ int64_t warp_sum[kCWarps + C::kPWarps];
-  __shared__ int start_n, start_g, start_blk, trouble;
+  __shared__ int start_n, start_len, start_g, start_blk, trouble;
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
@@ -215,13 +218,14 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     }
     mbar_init(&meet, 32 * kCWarps);
     fence_mbar_init();
-    trouble = start_n = start_g = start_blk = 0;
+    trouble = start_n = start_len = start_g = start_blk = 0;
   }
   // units before each thread's run of sequences
   const int per = (a.N + C::kThreads - 1) / C::kThreads;
   const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
-  int64_t sum = 0;
-  for (int n = n0; n < n1; ++n) sum += blocks_of(a, n);
+  const int len0 = n0 < n1 ? a.kv_lens[n0] : 0;     // kept: usually a thread's only one
+  int64_t sum = n0 < n1 ? blocks_of<kTok>(a, len0) : 0;
+  for (int n = n0 + 1; n < n1; ++n) sum += blocks_of<kTok>(a, a.kv_lens[n]);
   int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -242,15 +246,19 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   const int64_t r0 = c < nc ? c * U / nc : 0, r1 = c < nc ? (c + 1) * U / nc : 0;
   if (r1 > r0 && before <= r0 && r0 < before + sum * a.Hkv) {
     int64_t rem = r0 - before;
-    for (int n = n0; n < n1; ++n) {
-      const int64_t nb = blocks_of(a, n);
+    int len = len0;
+    for (int n = n0;;) {
+      const int64_t nb = blocks_of<kTok>(a, len);
       if (rem < nb * a.Hkv) {
         start_n = n;
+        start_len = len;
         start_g = (int)(rem / nb);
         start_blk = (int)(rem % nb);
         break;
       }
       rem -= nb * a.Hkv;
+      if (++n == n1) break;                         // only if lengths change during the call
+      len = a.kv_lens[n];
     }
   }
   __syncthreads();
@@ -271,9 +279,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
     // the unit whose rows are looked up: one ahead of the unit being copied, so
     // that the table's latency passes behind the copies
-    int n = start_n, g = start_g, blk = start_blk, len = 0, nb = 0;
+    int n = start_n, g = start_g, blk = start_blk, len = start_len, nb = 0;
     auto measure = [&] {
-      len = (int)min((int64_t)max(a.kv_lens[n], 0), cap);
+      len = (int)min((int64_t)max(len, 0), cap);
       nb = (int)(((int64_t)len + kTok - 1) / kTok);
     };
     int page[E], in_page[E];
@@ -327,11 +335,13 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           uint32_t any = 0;
           while (!any && n + 1 < a.N) {            // the next sequence with tokens
             const int m = n + 1 + lane;
-            any = __ballot_sync(0xffffffffu, m < a.N && blocks_of(a, m) > 0);
+            len = m < a.N ? a.kv_lens[m] : 0;
+            any = __ballot_sync(0xffffffffu, blocks_of<kTok>(a, len) > 0);
             n += any ? __ffs(any) : 32;
           }
           if (!any) u = r1;                        // only if lengths change during the call
-          else measure();
+          len = __shfl_sync(0xffffffffu, len, __ffs(any) - 1 & 31);
+          measure();
         }
       }
       if (u < r1) lookup();
@@ -403,8 +413,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     const int row = lane >> 2, qd = lane & 3;
     const int mj = lane >> 3, mi = lane & 7;
     // ldmatrix row addresses: matrix mj, row mi
-    const uint32_t k_off = (uint32_t)((warp * 16 + (mj & 1) * 8 + mi) * C::kRow + (mj >> 1) * 16);
-    const uint32_t v_off = (uint32_t)((warp * 16 + (mj >> 1) * 8 + mi) * C::kRow + (mj & 1) * 16);
+    const int tok0 = warp * 16 * C::kTiles;
+    const uint32_t k_off = (uint32_t)((tok0 + (mj & 1) * 8 + mi) * C::kRow + (mj >> 1) * 16);
+    const uint32_t v_off = (uint32_t)((tok0 + (mj >> 1) * 8 + mi) * C::kRow + (mj & 1) * 16);
     const uint32_t q_off = (uint32_t)(mi * C::kRow + mj * 16);    // two k-steps per load
     const uint32_t smb = smem_u32(sm);
     uint32_t qf[NT][D / 16][2];
@@ -437,49 +448,63 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           l[t][0] = l[t][1] = 0.f;
         }
       }
-      const int nt = b.ntok - warp * 16;       // this warp's tokens
+      const int nt = b.ntok - tok0;            // this warp's tokens (rows behind them are zeros)
       if (nt > 0) {
-        // fragments are loaded a batch ahead of the products that use them
-        constexpr int B = C::kBatch, KB = D / 16 / B;
-        float s[NT][B][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < B; ++e) s[t][e][0] = s[t][e][1] = s[t][e][2] = s[t][e][3] = 0.f;
+        // the fragments of all K tiles, then of all V tiles, in batches: one is
+        // loaded ahead of the products that use it
+        constexpr int TT = C::kTiles, B = C::kBatch, KB = D / 16 / B, NB = TT * KB;
         uint32_t fr[2][B][4];
+        auto load = [&](int i) {                   // batch i of 2 NB
+          const int tt = i / KB % TT, kb = i % KB;
+          const uint32_t at = base + tt * 16 * C::kRow + kb * B * 32;
 #pragma unroll
-        for (int i = 0; i < B; ++i) ldsm4(base + k_off + i * 32, fr[0][i]);
+          for (int e = 0; e < B; ++e) {
+            if (i < NB) ldsm4(at + k_off + e * 32, fr[i & 1][e]);
+            else ldsm4_t(at + C::kV + v_off + e * 32, fr[i & 1][e]);
+          }
+        };
+        load(0);
+        float x[TT][NT][4];                        // tokens row, row + 8; heads 2 qd, 2 qd + 1
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int tt = 0; tt < TT; ++tt) {
+          float s[NT][B][4];
 #pragma unroll
-          for (int i = 0; i < B; ++i) {
-            if (kb + 1 < KB)
-              ldsm4(base + k_off + ((kb + 1) * B + i) * 32, fr[(kb + 1) & 1][i]);
-            else                                   // the first V fragments, for after the softmax
-              ldsm4_t(base + C::kV + v_off + i * 32, fr[KB & 1][i]);
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < B; ++e) s[t][e][0] = s[t][e][1] = s[t][e][2] = s[t][e][3] = 0.f;
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            load(tt * KB + kb + 1);                // behind the last K batch: the first of V
+#pragma unroll
+            for (int e = 0; e < B; ++e)
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                mma16816<Th>(s[t][e], fr[(tt * KB + kb) & 1][e], qf[t][kb * B + e][0],
+                             qf[t][kb * B + e][1]);
           }
 #pragma unroll
-          for (int i = 0; i < B; ++i)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-              mma16816<Th>(s[t][i], fr[kb & 1][i], qf[t][kb * B + i][0], qf[t][kb * B + i][1]);
+            for (int e = 0; e < 4; ++e)
+              x[tt][t][e] = 16 * tt + row + 8 * (e >> 1) < nt ? total(s[t], e) * p.sl2 : -INFINITY;
         }
-        // scores of tokens row, row + 8 and heads 2 qd, 2 qd + 1
-        const bool in0 = row < nt, in1 = row + 8 < nt;
-        uint32_t hi[NT][2], lo[NT][2];
+        uint32_t hi[TT][NT][2], lo[TT][NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const int h0 = 8 * t + 2 * qd;
-          float x[4];
+          float top[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = (e < 2 ? in0 : in1) ? total(s[t], e) * p.sl2 : -INFINITY;
-          const bool rise = (h0 < p.G && fmaxf(x[0], x[2]) > m[t][0] + 8.f) ||
-                            (h0 + 1 < p.G && fmaxf(x[1], x[3]) > m[t][1] + 8.f);
+          for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(x[0][t][e], x[0][t][e + 2]);
+#pragma unroll
+            for (int tt = 1; tt < TT; ++tt) top[e] = fmaxf(top[e], fmaxf(x[tt][t][e], x[tt][t][e + 2]));
+          }
+          const int h0 = 8 * t + 2 * qd;
+          const bool rise = (h0 < p.G && top[0] > m[t][0] + 8.f) ||
+                            (h0 + 1 < p.G && top[1] > m[t][1] + 8.f);
           if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mb = fmaxf(x[e], x[e + 2]);
+              float mb = top[e];
               mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 4));
               mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 8));
               mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
@@ -497,34 +522,33 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           // a max of -inf (no finite score yet) must not meet itself
           const float ma = m[t][0] == -INFINITY ? 0.f : m[t][0];
           const float mb = m[t][1] == -INFINITY ? 0.f : m[t][1];
-          const float p0 = ex2(x[0] - ma), p1 = ex2(x[1] - mb);
-          const float p2 = ex2(x[2] - ma), p3 = ex2(x[3] - mb);
-          l[t][0] += p0 + p2;
-          l[t][1] += p1 + p3;
-          split2(p0, p1, Th(), hi[t][0], lo[t][0]);
-          split2(p2, p3, Th(), hi[t][1], lo[t][1]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            hi[t][e] = transpose8x8(hi[t][e]);
-            lo[t][e] = transpose8x8(lo[t][e]);
+          for (int tt = 0; tt < TT; ++tt) {
+            const float p0 = ex2(x[tt][t][0] - ma), p1 = ex2(x[tt][t][1] - mb);
+            const float p2 = ex2(x[tt][t][2] - ma), p3 = ex2(x[tt][t][3] - mb);
+            l[t][0] += p0 + p2;
+            l[t][1] += p1 + p3;
+            split2(p0, p1, Th(), hi[tt][t][0], lo[tt][t][0]);
+            split2(p2, p3, Th(), hi[tt][t][1], lo[tt][t][1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              hi[tt][t][e] = transpose8x8(hi[tt][t][e]);
+              lo[tt][t][e] = transpose8x8(lo[tt][t][e]);
+            }
           }
         }
 #pragma unroll
-        for (int vb = 0; vb < KB; ++vb) {
-          const uint32_t (&cur)[B][4] = fr[(KB + vb) & 1];
-          if (vb + 1 < KB) {
-#pragma unroll
-            for (int i = 0; i < B; ++i)
-              ldsm4_t(base + C::kV + v_off + ((vb + 1) * B + i) * 32, fr[(KB + vb + 1) & 1][i]);
-          }
+        for (int i = 0; i < NB; ++i) {
+          const int tt = i / KB, vb = i % KB;
+          if (i + 1 < NB) load(NB + i + 1);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int i = 0; i < B; ++i)
-              mma16816<Th>(o[t][vb * B + i], cur[i], hi[t][0], hi[t][1]);
+            for (int e = 0; e < B; ++e)
+              mma16816<Th>(o[t][vb * B + e], fr[(NB + i) & 1][e], hi[tt][t][0], hi[tt][t][1]);
 #pragma unroll
-            for (int i = 0; i < B; ++i)
-              mma16816<Th>(o[t][vb * B + i], cur[i], lo[t][0], lo[t][1]);
+            for (int e = 0; e < B; ++e)
+              mma16816<Th>(o[t][vb * B + e], fr[(NB + i) & 1][e], lo[tt][t][0], lo[tt][t][1]);
           }
         }
       }
@@ -604,48 +628,74 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 
 // Joins the pieces of the sequence (and key-value head) that CTA c of the split
 // kernel started and did not end; also sums up what the CTAs met.
+constexpr int kJoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
-  constexpr int kLanes = D / 4, kParts = 128 / kLanes;
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p) {
+  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;
+  __shared__ float weight[kMaxCtas];
   __shared__ float4 acc[kParts][kLanes];
-  __shared__ float sums[kParts];
+  __shared__ float red[kJoinThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedDecodeArgs& a = p.a;
-  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (c == 0 && h == 0) {
     int f = 0;
-    for (int i = tid; i < (int)gridDim.x; i += 128) f |= p.flag[i];
+    for (int i = tid; i < (int)gridDim.x; i += kJoinThreads) f |= p.flag[i];
     const int timeout = __syncthreads_or(f & 1), wrong = __syncthreads_or(f & 2);
     if (tid == 0) *p.status = timeout ? 1 : (wrong ? 2 : 0);
   }
   const int4 j = p.join[c];
   if (!j.w) return;
-  const int part = tid / kLanes, d = 4 * (tid % kLanes);
-  const int pieces = j.z - c + 1;
+  const int pieces = j.z - c + 1;             // at most the grid's CTAs
   auto at = [&](int i) { return ((int64_t)(c + i) * 2 + (i == 0)) * p.G + h; };
+  // weights of the pieces: all loads at once, then sums in a fixed order
+  float2 ml[kMaxCtas / kJoinThreads];
   float M = -INFINITY;
-  for (int i = 0; i < pieces; ++i) M = fmaxf(M, p.ml[at(i) * 2]);
-  float L = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / kJoinThreads; ++k) {
+    const int i = tid + k * kJoinThreads;
+    ml[k] = i < pieces ? *reinterpret_cast<const float2*>(p.ml + at(i) * 2)
+                       : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, ml[k].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / kJoinThreads; ++k) {
+    const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - M);
+    weight[tid + k * kJoinThreads] = f;
+    L += f * ml[k].y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  __syncthreads();
+  if (lane == 0) red[warp] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) L += red[w];
+  const int part = tid / kLanes, d = 4 * (tid % kLanes);
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
   for (int i = part; i < pieces; i += kParts) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.ml + at(i) * 2);
     const float4 v = *reinterpret_cast<const float4*>(p.po + at(i) * D + d);
-    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);
-    L += f * ml.y;
+    const float f = weight[i];
     y[0] += f * v.x;
     y[1] += f * v.y;
     y[2] += f * v.z;
     y[3] += f * v.w;
   }
   acc[part][tid % kLanes] = make_float4(y[0], y[1], y[2], y[3]);
-  if (tid % kLanes == 0) sums[part] = L;
   __syncthreads();
   if (part) return;
-  L = sums[0];
 #pragma unroll
   for (int i = 1; i < kParts; ++i) {
     const float4 v = acc[i][tid % kLanes];
-    L += sums[i];
     y[0] += v.x;
     y[1] += v.y;
     y[2] += v.z;
@@ -685,7 +735,7 @@ cudaError_t launch_split(const PagedParams& p, int sms) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, (unsigned)p.G);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = p.a.stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
