@@ -612,6 +612,8 @@ gdn_status gdn_paged_attention_decode(const void* q, int64_t q_row_stride, const
       !valid_dtype3(o_dtype) || !(scale == scale))
     return GDN_ERR_INVALID_ARG;
   if (H_q / H_kv > 16) return GDN_ERR_UNSUPPORTED;
+  // units of work are counted in 64 bits, times a few thousand
+  if ((double)N * H_kv * max_pages * page_size > 9e15) return GDN_ERR_UNSUPPORTED;
   const int64_t row = (int64_t)H_q * head_dim;
   if (q_row_stride < row || (gate && gate_row_stride < row) || max_pages <= 0 ||
       table_row_stride < max_pages || (int64_t)max_pages * page_size > INT32_MAX)

@@ -210,6 +210,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
+  // the join may take its place on the chip while this runs
+  asm volatile("griddepcontrol.launch_dependents;");
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -224,8 +226,13 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   const int per = (a.N + C::kThreads - 1) / C::kThreads;
   const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
   const int len0 = n0 < n1 ? a.kv_lens[n0] : 0;     // kept: usually a thread's only one
-  int64_t sum = n0 < n1 ? blocks_of<kTok>(a, len0) : 0;
-  for (int n = n0 + 1; n < n1; ++n) sum += blocks_of<kTok>(a, a.kv_lens[n]);
+  int64_t sum = 0;
+  bool odd_len = false;
+  for (int n = n0, len = len0; n < n1; ++n) {
+    if (n > n0) len = a.kv_lens[n];
+    sum += blocks_of<kTok>(a, len);
+    odd_len |= !len_ok(a, len);
+  }
   int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -234,6 +241,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
+  if (odd_len) atomicMax(&trouble, 2);
   int64_t before = incl - sum, U = 0;
 #pragma unroll
   for (int w = 0; w < kCWarps + C::kPWarps; ++w) {
@@ -288,11 +296,11 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     auto lookup = [&] {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int t = blk * kTok + row0 + lane + 32 * e;
+        const uint32_t t = (uint32_t)blk * kTok + row0 + lane + 32 * e;
         page[e] = -2;                              // no such row
-        if (t < len) {
-          const int j = t / a.page_size;
-          in_page[e] = t - j * a.page_size;
+        if (t < (uint32_t)len) {
+          const uint32_t j = t / (uint32_t)a.page_size;
+          in_page[e] = (int)(t - j * a.page_size);
           page[e] = a.table[(int64_t)n * a.table_row_stride + j];
           if (page[e] < 0 || page[e] >= a.num_pages) page[e] = -1;
         }
@@ -395,21 +403,6 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     if (!fine && lane == 0) atomicMax(&trouble, 3);
   } else {
     // ------------------------------------------------------------ compute --
-    // sequences without a token, or with a length out of range
-    for (int n = c; n < a.N; n += gridDim.x) {
-      const int len = a.kv_lens[n];
-      const bool ok = len_ok(a, len);
-      if (ok && len > 0) continue;
-      if (!ok && tid == 0) atomicMax(&trouble, 2);
-      const float v = ok ? 0.f : __int_as_float(0x7fc00000);
-      for (int i = tid; i < a.Hq * D / 4; i += 32 * kCWarps) {
-        float y[4] = {v, v, v, v};
-        put_out(a, (int64_t)n * a.Hq + i / (D / 4), n, i / (D / 4), 4 * (i % (D / 4)), y);
-      }
-      if (a.lse)
-        for (int h = tid; h < a.Hq; h += 32 * kCWarps)
-          a.lse[(int64_t)n * a.Hq + h] = ok ? -INFINITY : v;
-    }
     const int row = lane >> 2, qd = lane & 3;
     const int mj = lane >> 3, mi = lane & 7;
     // ldmatrix row addresses: matrix mj, row mi
@@ -621,7 +614,6 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     }
     if (dead) atomicMax(&trouble, 3);           // a wait ran out: more than bad input
   }
-  asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   if (tid == 0) p.flag[c] = trouble == 3 ? 1 : trouble;
 }
@@ -635,9 +627,23 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   __shared__ float weight[kMaxCtas];
   __shared__ float4 acc[kParts][kLanes];
   __shared__ float red[kJoinThreads / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedDecodeArgs& a = p.a;
   const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // sequences without a token, or with a length out of range: nothing of the
+  // split kernel's is needed for them
+  for (int n = c; n < a.N; n += gridDim.x) {
+    const int len = a.kv_lens[n];
+    const bool ok = len_ok(a, len);
+    if (ok && len > 0) continue;
+    const float v = ok ? 0.f : __int_as_float(0x7fc00000);
+    for (int i = tid; i < a.Hkv * (D / 4); i += kJoinThreads) {
+      const int hq = i / (D / 4) * p.G + h, d = 4 * (i % (D / 4));
+      float y[4] = {v, v, v, v};
+      put_out(a, (int64_t)n * a.Hq + hq, n, hq, d, y);
+      if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = ok ? -INFINITY : v;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c == 0 && h == 0) {
     int f = 0;
     for (int i = tid; i < (int)gridDim.x; i += kJoinThreads) f |= p.flag[i];
