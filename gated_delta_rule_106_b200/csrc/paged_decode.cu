@@ -40,7 +40,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kCWarps = 4;                  // computing warps
-constexpr int kMaxCtas = 512;
+constexpr int kPhases = 3;                  // see Ranges
+constexpr int kMaxBase = 2 * 160;           // CTAs at once
+constexpr int kMaxRanges = kPhases * kMaxBase;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 template <int D, int NT>
@@ -52,29 +54,73 @@ struct Cfg {
   static constexpr int kV = kTok * kRow;              // offsets within a stage
   static constexpr int kQ = 2 * kTok * kRow;
   static constexpr int kStage = kQ + kHeads * kRow;
-  static constexpr int kPWarps = 4;                   // copying warps, half for K, half for V
+  // copying warps, half for K, half for V: at D = 128 a row is half a warp's copy
+  // and its lookup counts more
+  static constexpr int kPWarps = D == 128 && NT == 1 ? 8 : 4;
   static constexpr int kThreads = 32 * (kCWarps + kPWarps);
+  static constexpr int kRuns = D == 64 ? 64 : 256;      // runs of sequences that are summed
   static constexpr int kCtasPerSm = D == 64 && NT == 1 ? 2 : 1;
   static constexpr int kStages = D == 64 && NT == 2 ? 5 : 3;
   static constexpr int kSmem = kStages * kStage;
   static constexpr int kBatch = D == 256 && NT == 2 ? 2 : 4;   // fragments loaded ahead
   static constexpr int kPad = D + 4;                  // floats per head when pieces meet
+  // two CTAs per SM: 228 KB with 1 KB of the system's and ~1.5 KB of barriers and sums each
+  static_assert(kCtasPerSm == 1 || kSmem + 2560 <= 114 * 1024, "two CTAs fit");
   static_assert(kCWarps * kHeads * kPad * 4 <= kQ, "pieces meet in a block's K and V rows");
 };
 
 enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
 
-struct BlockDesc { int n, g, ntok, flags, piece, pad[3]; };   // piece: -1 or 0 / 1
+struct BlockDesc { int n, g, ntok, flags, piece, range, pad[2]; };   // piece: -1 or 0 / 1
+
+// How the U units are cut into ranges, in order: `base` (the CTAs that run at
+// once) equal ranges that hold 34 of 40 parts of the work, then base ranges with
+// 4 and base with 2 parts, which go to whoever is done: SMs differ by 10 % in the
+// bandwidth they get. Below 64 units per CTA the extra pieces cost more than that
+// (1 x 131071 tokens, 55 units: 102 us against 94), and there is one phase.
+constexpr int kStealUnits = 64;
+struct Ranges {
+  int64_t U, q;               // U = q * 40 base + r
+  int base, phases, r;
+  __device__ Ranges(int64_t units, int ctas, bool steal) : U(units), base(ctas), phases(1) {
+    if (steal && units >= kStealUnits * (int64_t)ctas) phases = 3;
+    else base = max((int)min((int64_t)ctas, units), 1);
+    if (units <= INT32_MAX) {
+      q = (uint32_t)units / (uint32_t)(40 * base);
+    } else {
+      q = units / (40 * base);
+    }
+    r = (int)(units - q * (40 * base));
+  }
+  // parts of 40 behind phase ph
+  __device__ int rest(int ph) const { return ph == 0 ? 40 : (ph >= phases ? 0 : 10 - 4 * ph); }
+  // first unit of range v, U * part / (40 base) (U behind the last range)
+  __device__ int64_t start(int v) const {
+    if (v >= phases * base) return U;
+    const int ph = v < base ? 0 : (v < 2 * base ? 1 : 2), i = v - ph * base;
+    const int part = (40 - rest(ph)) * base + (rest(ph) - rest(ph + 1)) * i;
+    return q * part + (uint32_t)(r * part) / (uint32_t)(40 * base);   // r, part < 40 * 320
+  }
+  // the range of unit x: the last v with start(v) <= x
+  __device__ int of(int64_t x) const {
+    const int64_t most = ((x + 1) * 40 * base - 1) / U;
+    int ph = 0;
+    while (ph + 1 < phases && (int64_t)(40 - rest(ph + 1)) * base <= most) ++ph;
+    const int64_t i = (most - (int64_t)(40 - rest(ph)) * base) / (rest(ph) - rest(ph + 1));
+    return ph * base + (int)min(i, (int64_t)base - 1);
+  }
+};
 
 struct PagedParams {
   PagedDecodeArgs a;
   int G;
   float sl2;               // scale * log2(e)
   int* status;             // workspace word 0
-  int* flag;               // [kMaxCtas] what each CTA met: 0, 1 (a wait ran out), 2 (bad input)
-  int4* join;              // [kMaxCtas] {n, g, last CTA, 1} for the sequence piece that starts there
-  float* ml;               // [kMaxCtas][2][G][2]
-  float* po;               // [kMaxCtas][2][G][D]
+  int base;                // CTAs that run at once; more in the grid are taken over
+  int* flag;               // [grid] what each CTA met: 0, 1 (a wait ran out), 2 (bad input)
+  int4* join;              // [grid] {n, g, last range, 1} for the piece that starts in a range
+  float* ml;               // [grid][2][G][2]
+  float* po;               // [grid][2][G][D]
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -92,6 +138,29 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+// Asks the hardware for a CTA of this grid that has not started; the answer
+// (16 bytes) lands on `bar`.
+__device__ __forceinline__ void ask_cta(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(smem_u32(answer)), "r"(smem_u32(bar))
+      : "memory");
+}
+// The CTA that the answer gives us, or -1: none is left.
+__device__ __forceinline__ int given_cta(const uint4* answer) {
+  int id;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(id)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return id;
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -157,31 +226,31 @@ __device__ __forceinline__ int blocks_of(const PagedDecodeArgs& a, int len) {
   return len_ok(a, len) ? (int)(((int64_t)len + TOK - 1) / TOK) : 0;
 }
 
-// four output values of one (sequence, head): gate and round
+// V = 2 or 4 output values of one (sequence, head): gate and round
+template <int V>
 __device__ __forceinline__ void put_out(const PagedDecodeArgs& a, int64_t row, int n, int h,
-                                        int d, float (&y)[4]) {
+                                        int d, float (&y)[V]) {
   if (a.gate) {
-    const uint2 u = *reinterpret_cast<const uint2*>(
+    const __nv_bfloat162* g = reinterpret_cast<const __nv_bfloat162*>(
         static_cast<const __nv_bfloat16*>(a.gate) + n * a.gate_row_stride + (int64_t)h * a.D + d);
-    const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-    const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    y[0] /= 1.0f + __expf(-g0.x);
-    y[1] /= 1.0f + __expf(-g0.y);
-    y[2] /= 1.0f + __expf(-g1.x);
-    y[3] /= 1.0f + __expf(-g1.y);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 v = __bfloat1622float2(g[i]);
+      y[2 * i] /= 1.0f + __expf(-v.x);
+      y[2 * i + 1] /= 1.0f + __expf(-v.y);
+    }
   }
   const int64_t at = row * a.D + d;
-  if (a.o_dtype == GDN_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) =
-        make_float4(y[0], y[1], y[2], y[3]);
-  } else if (a.o_dtype == GDN_F16) {
-    __half2* o = reinterpret_cast<__half2*>(static_cast<__half*>(a.o) + at);
-    o[0] = __floats2half2_rn(y[0], y[1]);
-    o[1] = __floats2half2_rn(y[2], y[3]);
-  } else {
-    __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.o) + at);
-    o[0] = __floats2bfloat162_rn(y[0], y[1]);
-    o[1] = __floats2bfloat162_rn(y[2], y[3]);
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if (a.o_dtype == GDN_F32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.o) + at + i) = make_float2(y[i], y[i + 1]);
+    else if (a.o_dtype == GDN_F16)
+      *reinterpret_cast<__half2*>(static_cast<__half*>(a.o) + at + i) =
+          __floats2half2_rn(y[i], y[i + 1]);
+    else
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.o) + at + i) =
+          __floats2bfloat162_rn(y[i], y[i + 1]);
   }
 }
 
@@ -206,10 +275,13 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   __shared__ int wrong_page[C::kStages][C::kPWarps];    // met by each copying warp
   __shared__ float2 piece_ml[kCWarps][C::kHeads];
   __shared__ int64_t warp_sum[kCWarps + C::kPWarps];
-  __shared__ int start_n, start_len, start_g, start_blk, trouble;
+  __shared__ int64_t run_before[C::kRuns];         // units before each run of sequences
+  __shared__ int run_len[C::kRuns];                // length of the run's first sequence
+  __shared__ __align__(16) uint4 answer;
+  __shared__ uint64_t asked_full, asked_free;
+  __shared__ int trouble;
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = blockIdx.x;
   // the join may take its place on the chip while this runs
   asm volatile("griddepcontrol.launch_dependents;");
 
@@ -219,13 +291,15 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       mbar_init(&empty[i], kCWarps);
     }
     mbar_init(&meet, 32 * kCWarps);
+    mbar_init(&asked_full, 1);
+    mbar_init(&asked_free, C::kPWarps);
     fence_mbar_init();
-    trouble = start_n = start_len = start_g = start_blk = 0;
+    trouble = 0;
   }
-  // units before each thread's run of sequences
-  const int per = (a.N + C::kThreads - 1) / C::kThreads;
+  const int per = (a.N + C::kRuns - 1) / C::kRuns;  // a run per thread, the first kRuns threads
   const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
-  const int len0 = n0 < n1 ? a.kv_lens[n0] : 0;     // kept: usually a thread's only one
+  const int len0 = n0 < n1 ? a.kv_lens[n0] : 0;
+  if (tid < C::kRuns) run_len[tid] = len0;
   int64_t sum = 0;
   bool odd_len = false;
   for (int n = n0, len = len0; n < n1; ++n) {
@@ -248,27 +322,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     if (w < warp) before += warp_sum[w];
     U += warp_sum[w];
   }
-  before *= a.Hkv;
+  if (tid < C::kRuns) run_before[tid] = before * a.Hkv;
   U *= a.Hkv;
-  const int64_t nc = min((int64_t)gridDim.x, U);    // CTAs that have a unit
-  const int64_t r0 = c < nc ? c * U / nc : 0, r1 = c < nc ? (c + 1) * U / nc : 0;
-  if (r1 > r0 && before <= r0 && r0 < before + sum * a.Hkv) {
-    int64_t rem = r0 - before;
-    int len = len0;
-    for (int n = n0;;) {
-      const int64_t nb = blocks_of<kTok>(a, len);
-      if (rem < nb * a.Hkv) {
-        start_n = n;
-        start_len = len;
-        start_g = (int)(rem / nb);
-        start_blk = (int)(rem % nb);
-        break;
-      }
-      rem -= nb * a.Hkv;
-      if (++n == n1) break;                         // only if lengths change during the call
-      len = a.kv_lens[n];
-    }
-  }
+  const Ranges ranges(U, p.base, (int)gridDim.x > p.base);
   __syncthreads();
 
   if (warp >= kCWarps) {
@@ -283,11 +339,15 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     const PageStrides cs = is_v ? a.vs : a.ks;
     const uint32_t dst0 = smem_u32(sm) + (is_v ? C::kV : 0) +
                           (row0 + lane / LPR) * C::kRow + (lane % LPR) * 16;
-    if (tid == 32 * kCWarps) p.join[c] = make_int4(0, 0, 0, 0);
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
-    // the unit whose rows are looked up: one ahead of the unit being copied, so
-    // that the table's latency passes behind the copies
-    int n = start_n, g = start_g, blk = start_blk, len = start_len, nb = 0;
+    // the unit whose rows are looked up, one ahead of the unit being copied, so
+    // that the table's latency passes behind the copies: range, units to its end,
+    // sequence, key-value head, block; the sequence's length and blocks
+    int range = blockIdx.x, n = 0, g = 0, blk = 0, len = 0, nb = 0;
+    int64_t u = 0, r1 = 0;
+    bool first = true, begins = true, bad = false;
+    bool steal = (int)gridDim.x > p.base, asked = false, late = false;
+    int answers = 0;
     auto measure = [&] {
       len = (int)min((int64_t)max(len, 0), cap);
       nb = (int)(((int64_t)len + kTok - 1) / kTok);
@@ -306,13 +366,87 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         }
       }
     };
-    if (r1 > r0) {
+    // go to the first unit of `range`
+    auto enter = [&] {
+      u = ranges.start(range);
+      r1 = ranges.start(range + 1);
+      if (lead && lane == 0) {
+        p.join[range] = make_int4(0, 0, 0, 0);
+        if (range != (int)blockIdx.x) p.flag[range] = 0;   // that CTA never starts
+      }
+      if (u >= r1) return;
+      // the last run of sequences that starts at or before u ...
+      int at = 0;
+#pragma unroll
+      for (int k = 0; k < C::kRuns / 32; ++k) at += run_before[lane * (C::kRuns / 32) + k] <= u;
+      at = __reduce_add_sync(0xffffffffu, at) - 1;
+      // ... and the sequence in it
+      int64_t rem = u - run_before[at];
+      n = at * per;
+      if (per == 1) {
+        len = run_len[at];
+      } else {
+        for (;; n += 32) {
+          const int m = n + lane;
+          len = m < a.N && m < (at + 1) * per ? a.kv_lens[m] : 0;
+          const int64_t units = (int64_t)blocks_of<kTok>(a, len) * a.Hkv;
+          int64_t upto = units;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, upto > rem);
+          if (past || n + 32 >= (at + 1) * per) {  // without a hit: lengths change during the call
+            const int src = past ? __ffs(past) - 1 : 0;
+            rem -= __shfl_sync(0xffffffffu, upto - units, src);
+            len = __shfl_sync(0xffffffffu, len, src);
+            n = min(n + src, a.N - 1);
+            break;
+          }
+          rem -= __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
       measure();
-      lookup();
-    }
-    bool first = true, bad = false, begins = blk == 0;
+      if (nb == 0) { u = r1; return; }             // lengths change during the call
+      if (rem <= INT32_MAX) {
+        g = (int)((uint32_t)rem / (uint32_t)nb);
+        blk = (int)rem - g * nb;
+      } else {
+        g = (int)(rem / nb);
+        blk = (int)(rem % nb);
+      }
+      g = min(g, a.Hkv - 1);
+      begins = blk == 0;
+      first = true;
+    };
+    auto ask = [&] {
+      if (lead && lane == 0) {
+        if (answers > 0 && !mbar_wait_bounded(&asked_free, (answers - 1) & 1, kLimitNs)) late = true;
+        else ask_cta(&answer, &asked_full);
+      }
+      asked = true;
+    };
+    // when a range is done, take over CTAs that have not started until one has units
+    auto refill = [&] {
+      while (u >= r1 && steal) {
+        if (!asked) ask();
+        if (!mbar_wait_bounded(&asked_full, answers & 1, kLimitNs)) { late = true; break; }
+        range = given_cta(&answer);
+        asked = false;
+        ++answers;
+        fence_proxy_async_smem();                  // read here before the next answer lands
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&asked_free);
+        if (range < 0) steal = false;
+        else enter();
+      }
+    };
+    enter();
+    refill();
+    if (u < r1) lookup();
     int it = 0;
-    for (int64_t u = r0; u < r1; ++it) {
+    for (; u < r1; ++it) {
       const int st = it % C::kStages;
       int64_t off[E];
       bool wrong = false;
@@ -322,19 +456,23 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         wrong |= page[e] == -1;
       }
       bad |= __any_sync(0xffffffffu, wrong);       // a warp's own rows
+      const bool bad_now = bad, first_now = first;
       const bool last_blk = blk + 1 == nb, last = last_blk || u + 1 == r1;
       BlockDesc b;
       b.n = n;
       b.g = g;
       b.ntok = min(kTok, len - blk * kTok);
       b.flags = (first ? kFirst : 0) | (last ? kLast : 0);
-      // whole in this CTA: straight to the output; the piece that a CTA
+      // whole in this range: straight to the output; the piece that a range
       // continues goes to slot 0, the one that it starts to slot 1
       b.piece = begins ? (last_blk ? -1 : 1) : 0;
+      b.range = range;
       const int64_t end = u + (nb - blk);          // unit behind this sequence and head
-      // on to the next unit
+      // on to the next unit; a range's successor is asked for shortly before its end
       ++u;
       ++blk;
+      first = last;
+      if (last) bad = false;
       if (last_blk) {
         blk = 0;
         begins = true;
@@ -348,10 +486,12 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             n += any ? __ffs(any) : 32;
           }
           if (!any) u = r1;                        // only if lengths change during the call
-          len = __shfl_sync(0xffffffffu, len, __ffs(any) - 1 & 31);
+          len = __shfl_sync(0xffffffffu, len, (__ffs(any) - 1) & 31);
           measure();
         }
       }
+      if (steal && !asked && r1 - u <= 3) ask();
+      refill();
       if (u < r1) lookup();
       if (!mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs)) break;
       const uint32_t dst = dst0 + st * C::kStage;
@@ -371,7 +511,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           cp_async16(dst + (r0 + i * RPI) * C::kRow,
                      cache + max(o[i], (int64_t)0) + (lane % LPR) * 8, o[i] >= 0);
       }
-      if (lead && first) {
+      if (lead && first_now) {
         const Th* q = static_cast<const Th*>(a.q) + b.n * a.q_row_stride + (int64_t)b.g * p.G * D;
         for (int i = lane; i < p.G * LPR; i += 32)
           cp_async16(smem_u32(sm) + st * C::kStage + C::kQ + (i / LPR) * C::kRow +
@@ -381,15 +521,13 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         if (lead) {
           desc[st] = b;
           if (last && b.piece == 1)
-            p.join[c] = make_int4(b.n, b.g, (int)((end * nc - 1) / U), 1);
+            p.join[b.range] = make_int4(b.n, b.g, ranges.of(end - 1), 1);
         }
-        wrong_page[st][warp - kCWarps] = bad;
-        if (bad) atomicMax(&trouble, 2);
+        wrong_page[st][warp - kCWarps] = bad_now;
+        if (bad_now) atomicMax(&trouble, 2);
         mbar_arrive(&full[st]);
       }
       cp_async_arrive(&full[st]);
-      first = last;
-      if (last) bad = false;
     }
     // end mark, then wait for the copies in flight
     const int st = it % C::kStages;
@@ -400,7 +538,10 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       mbar_arrive(&full[st]);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!fine && lane == 0) atomicMax(&trouble, 3);
+    // an answer that nobody waited for (only after a wait ran out)
+    if (asked && lead && lane == 0 && !late)
+      late = !mbar_wait_bounded(&asked_full, answers & 1, kLimitNs);
+    if ((!fine || late) && lane == 0) atomicMax(&trouble, 3);
   } else {
     // ------------------------------------------------------------ compute --
     const int row = lane >> 2, qd = lane & 3;
@@ -600,10 +741,10 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             const float inv = 1.f / L;
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] *= inv;
-            put_out(a, (int64_t)b.n * a.Hq + hq, b.n, hq, d, y);
+            put_out<4>(a, (int64_t)b.n * a.Hq + hq, b.n, hq, d, y);
             if (a.lse && d == 0) a.lse[(int64_t)b.n * a.Hq + hq] = (M + log2f(L)) * kLn2;
           } else {
-            const int64_t at = ((int64_t)c * 2 + b.piece) * p.G + h;
+            const int64_t at = ((int64_t)b.range * 2 + b.piece) * p.G + h;
             *reinterpret_cast<float4*>(p.po + at * D + d) = make_float4(y[0], y[1], y[2], y[3]);
             if (d == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, L);
           }
@@ -615,23 +756,25 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     if (dead) atomicMax(&trouble, 3);           // a wait ran out: more than bad input
   }
   __syncthreads();
-  if (tid == 0) p.flag[c] = trouble == 3 ? 1 : trouble;
+  if (tid == 0) p.flag[blockIdx.x] = trouble == 3 ? 1 : trouble;
 }
 
-// Joins the pieces of the sequence (and key-value head) that CTA c of the split
-// kernel started and did not end; also sums up what the CTAs met.
-constexpr int kJoinThreads = 256;
+// Joins the pieces of sequences (and key-value heads) that start in one range
+// and end in a later one; also sums up what the CTAs met. A warp takes one
+// range and head; where a sequence has many pieces (a long one, alone), the
+// block's warps share them.
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kFewPieces = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p) {
-  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;
-  __shared__ float weight[kMaxCtas];
-  __shared__ float4 acc[kParts][kLanes];
-  __shared__ float red[kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int ranges) {
+  constexpr int V = D == 64 ? 2 : 4, K = D / 32 / V;       // a lane's K vectors of V floats
+  __shared__ float acc[kJoinWarps][D];
+  __shared__ int4 entry[kJoinWarps];
   const PagedDecodeArgs& a = p.a;
-  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c0 = blockIdx.x * kJoinWarps, h = blockIdx.y;
   // sequences without a token, or with a length out of range: nothing of the
   // split kernel's is needed for them
-  for (int n = c; n < a.N; n += gridDim.x) {
+  for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
     const int len = a.kv_lens[n];
     const bool ok = len_ok(a, len);
     if (ok && len > 0) continue;
@@ -639,86 +782,130 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     for (int i = tid; i < a.Hkv * (D / 4); i += kJoinThreads) {
       const int hq = i / (D / 4) * p.G + h, d = 4 * (i % (D / 4));
       float y[4] = {v, v, v, v};
-      put_out(a, (int64_t)n * a.Hq + hq, n, hq, d, y);
+      put_out<4>(a, (int64_t)n * a.Hq + hq, n, hq, d, y);
       if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = ok ? -INFINITY : v;
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c == 0 && h == 0) {
+  if (blockIdx.x == 0 && h == 0) {
     int f = 0;
-    for (int i = tid; i < (int)gridDim.x; i += kJoinThreads) f |= p.flag[i];
+    for (int i = tid; i < ranges; i += kJoinThreads) f |= p.flag[i];
     const int timeout = __syncthreads_or(f & 1), wrong = __syncthreads_or(f & 2);
     if (tid == 0) *p.status = timeout ? 1 : (wrong ? 2 : 0);
   }
-  const int4 j = p.join[c];
-  if (!j.w) return;
-  const int pieces = j.z - c + 1;             // at most the grid's CTAs
-  auto at = [&](int i) { return ((int64_t)(c + i) * 2 + (i == 0)) * p.G + h; };
-  // weights of the pieces: all loads at once, then sums in a fixed order
-  float2 ml[kMaxCtas / kJoinThreads];
-  float M = -INFINITY;
+  // one warp's sum over pieces first, first + step, ...; returns the max and sum
+  // over all pieces. Loads go out several at a time.
+  auto gather = [&](int c, const int4& j, int first, int step, float (&y)[K][V]) -> float2 {
+    const int pieces = j.z - c + 1;
+    auto at = [&](int i) { return ((int64_t)(c + i) * 2 + (i == 0)) * p.G + h; };
+    auto weight = [](float m, float M) { return m == -INFINITY ? 1.f : ex2(m - M); };
+    float M = -INFINITY, L = 0.f;
+    for (int i0 = lane; i0 < pieces; i0 += 128) {
+      float2 ml[4];
+      float top = M;
 #pragma unroll
-  for (int k = 0; k < kMaxCtas / kJoinThreads; ++k) {
-    const int i = tid + k * kJoinThreads;
-    ml[k] = i < pieces ? *reinterpret_cast<const float2*>(p.ml + at(i) * 2)
-                       : make_float2(-INFINITY, 0.f);
-    M = fmaxf(M, ml[k].x);
+      for (int e = 0; e < 4; ++e) {
+        ml[e] = i0 + 32 * e < pieces ? *reinterpret_cast<const float2*>(p.ml + at(i0 + 32 * e) * 2)
+                                     : make_float2(-INFINITY, 0.f);
+        top = fmaxf(top, ml[e].x);
+      }
+      L *= weight(M, top);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) L += weight(ml[e].x, top) * ml[e].y;
+      M = top;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+      const float top = fmaxf(M, m2);
+      const float a1 = weight(M, top) * L, a2 = weight(m2, top) * l2;
+      L = lane & o ? a2 + a1 : a1 + a2;            // the same order in both lanes
+      M = top;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[k][e] = 0.f;
+    constexpr int R = kFewPieces;
+    for (int i0 = first; i0 < pieces; i0 += R * step) {
+      float m[R], v[R][K][V];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool live = i0 + r * step < pieces;
+        const int64_t x = at(live ? i0 + r * step : i0);
+        m[r] = live ? p.ml[x * 2] : INFINITY;
+        const float* src = p.po + x * D + lane * V;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if constexpr (V == 4)
+            *reinterpret_cast<float4*>(v[r][k]) = *reinterpret_cast<const float4*>(src + k * 32 * V);
+          else
+            *reinterpret_cast<float2*>(v[r][k]) = *reinterpret_cast<const float2*>(src + k * 32 * V);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (i0 + r * step < pieces) {
+          const float f = weight(m[r], M);
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[k][e] += f * v[r][k][e];
+        }
+      }
+    }
+    return make_float2(M, L);
+  };
+  auto finish = [&](const int4& j, float2 ml, float (&y)[K][V]) {
+    const int hq = j.y * p.G + h;
+    const int64_t row = (int64_t)j.x * a.Hq + hq;
+    const float inv = 1.f / ml.y;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[k][e] *= inv;
+      put_out<V>(a, row, j.x, hq, (k * 32 + lane) * V, y[k]);
+    }
+    if (a.lse && lane == 0) a.lse[row] = (ml.x + log2f(ml.y)) * kLn2;
+  };
+  const int4 none = make_int4(0, 0, 0, 0);
+  const int c = c0 + warp;
+  const int4 mine = c < ranges ? p.join[c] : none;
+  if (lane == 0) entry[warp] = mine;
+  const bool many = mine.w && mine.z - c + 1 > kFewPieces;
+  float y[K][V];
+  if (mine.w && !many) {
+    const float2 ml = gather(c, mine, 0, 1, y);
+    finish(mine, ml, y);
   }
+  if (!__syncthreads_or(many)) return;
+  for (int w = 0; w < kJoinWarps && c0 + w < ranges; ++w) {
+    const int4 j = entry[w];
+    if (!j.w || j.z - (c0 + w) + 1 <= kFewPieces) continue;
+    const float2 ml = gather(c0 + w, j, warp, kJoinWarps, y);
+    __syncthreads();                           // the last turn's sums are read
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[warp] = M;
-  __syncthreads();
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
-  float L = 0.f;
+      for (int e = 0; e < V; ++e) acc[warp][(k * 32 + lane) * V + e] = y[k][e];
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-  for (int k = 0; k < kMaxCtas / kJoinThreads; ++k) {
-    const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - M);
-    weight[tid + k * kJoinThreads] = f;
-    L += f * ml[k].y;
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          for (int i = 1; i < kJoinWarps; ++i) y[k][e] += acc[i][(k * 32 + lane) * V + e];
+      finish(j, ml, y);
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  __syncthreads();
-  if (lane == 0) red[warp] = L;
-  __syncthreads();
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) L += red[w];
-  const int part = tid / kLanes, d = 4 * (tid % kLanes);
-  float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = part; i < pieces; i += kParts) {
-    const float4 v = *reinterpret_cast<const float4*>(p.po + at(i) * D + d);
-    const float f = weight[i];
-    y[0] += f * v.x;
-    y[1] += f * v.y;
-    y[2] += f * v.z;
-    y[3] += f * v.w;
-  }
-  acc[part][tid % kLanes] = make_float4(y[0], y[1], y[2], y[3]);
-  __syncthreads();
-  if (part) return;
-#pragma unroll
-  for (int i = 1; i < kParts; ++i) {
-    const float4 v = acc[i][tid % kLanes];
-    y[0] += v.x;
-    y[1] += v.y;
-    y[2] += v.z;
-    y[3] += v.w;
-  }
-  const float inv = 1.f / L;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] *= inv;
-  const int hq = j.y * p.G + h;
-  put_out(a, (int64_t)j.x * a.Hq + hq, j.x, hq, d, y);
-  if (a.lse && d == 0) a.lse[(int64_t)j.x * a.Hq + hq] = (M + log2f(L)) * kLn2;
 }
 
-constexpr size_t kHeadBytes = 256 + kMaxCtas * 4 + kMaxCtas * 16;
+// most ranges of a launch: D = 64 has two CTAs per SM
+constexpr int max_ranges(int D) { return D == 64 ? kMaxRanges : kMaxRanges / 2; }
+constexpr size_t kHeadBytes = 256 + kMaxRanges * 4 + kMaxRanges * 16;
 
 template <int D, int NT, class Th>
-cudaError_t launch_split(const PagedParams& p, int sms) {
+cudaError_t launch_split(PagedParams p, int sms) {
   using C = Cfg<D, NT>;
   static std::atomic<uint64_t> ready{0};      // devices whose shared-memory limit is raised
   int dev = 0;
@@ -731,7 +918,11 @@ cudaError_t launch_split(const PagedParams& p, int sms) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int grid = min(sms * C::kCtasPerSm, kMaxCtas);
+  p.base = min(sms * C::kCtasPerSm, max_ranges(D) / kPhases);
+  // ranges to take over only where the tables have room for enough units
+  const int64_t cap = (int64_t)p.a.max_pages * p.a.page_size;
+  const int64_t most = (cap + C::kTok - 1) / C::kTok * p.a.N * p.a.Hkv;
+  const int grid = most >= kStealUnits * (int64_t)p.base ? kPhases * p.base : p.base;
   paged_split_kernel<D, NT, Th><<<grid, C::kThreads, C::kSmem, p.a.stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -740,12 +931,12 @@ cudaError_t launch_split(const PagedParams& p, int sms) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)p.G);
+  cfg.gridDim = dim3((unsigned)((grid + kJoinWarps - 1) / kJoinWarps), (unsigned)p.G);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = p.a.stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, grid);
 }
 
 template <int D, class Th>
@@ -762,7 +953,7 @@ cudaError_t launch_dim(const PagedParams& p, int sms) {
 }  // namespace
 
 size_t paged_decode_workspace(int group, int D) {
-  return kHeadBytes + (size_t)kMaxCtas * 2 * group * (D + 2) * 4;
+  return kHeadBytes + (size_t)max_ranges(D) * 2 * group * (D + 2) * 4;
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a) {
@@ -778,9 +969,9 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a) {
   p.sl2 = a.scale * 1.4426950408889634f;
   p.status = reinterpret_cast<int*>(ws);
   p.flag = reinterpret_cast<int*>(ws + 256);
-  p.join = reinterpret_cast<int4*>(ws + 256 + kMaxCtas * 4);
+  p.join = reinterpret_cast<int4*>(ws + 256 + kMaxRanges * 4);
   p.po = reinterpret_cast<float*>(ws + kHeadBytes);
-  p.ml = p.po + (size_t)kMaxCtas * 2 * p.G * a.D;
+  p.ml = p.po + (size_t)max_ranges(a.D) * 2 * p.G * a.D;
   return a.kv_dtype == GDN_F16 ? launch_dim<__half>(p, sms) : launch_dim<__nv_bfloat16>(p, sms);
 }
 
