@@ -13,17 +13,19 @@
 // pos * inv_freq is off by 2^-5 of a radian already. cos and sin then need 32
 // bits only.
 //
-// A CTA takes a few tokens with all their heads, so each (cos, sin) is made
-// once for all heads of its token. D / 8 lanes hold a row, 8 elements each.
+// A warp takes a token and a share of its heads (all of them where there are
+// tokens enough to fill the chip). D / 8 lanes hold a row, 8 elements each, so a
+// lane meets the same dims in every head: it makes its (cos, sin) and loads its
+// weights once and keeps them in registers, while several rows are in flight.
+// There is no barrier.
 #include "gdn_common.cuh"
 #include "launch.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTok = 4;                 // tokens per CTA
 
 __device__ __forceinline__ float to_f32(const void* w, gdn_dtype t, int i) {
   if (t == GDN_F32) return static_cast<const float*>(w)[i];
@@ -57,104 +59,149 @@ __device__ __forceinline__ float2 turn(double inv_freq, int pos, float scale) {
 }
 
 template <class Tx, class To, int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeArgs p, int tok) {
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeArgs p, int shares,
+                                                                int share_rows) {
   constexpr int LPR = D / 8;               // lanes per row
-  constexpr int RPW = 32 / LPR;            // rows per warp
-  extern __shared__ float2 cs[];           // [tok][R / 2]
-  __shared__ float stage[kWarps][256];     // rows being turned
-  __shared__ int64_t k_at[kMaxTok], v_at[kMaxTok];
-  __shared__ int live_at[kMaxTok];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int RPW = 32 / LPR;            // rows per warp and pass
+  constexpr int U = sizeof(Tx) == 4 ? 2 : 4;       // passes in flight
+  __shared__ float stage[kWarps][256];     // rows being turned, see below
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, l = lane % LPR;
-  const int64_t t0 = (int64_t)blockIdx.x * tok;
+  const int64_t task = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t t = task / shares;
+  if (t >= p.T) return;
+  const int Hq = p.q ? p.Hq : 0, Hkv = p.k ? p.Hkv : 0, H = Hq + 2 * Hkv;
+  const int first = (int)(task - t * shares) * share_rows, end = min(first + share_rows, H);
+
+  const int64_t slot = p.slot_map ? p.slot_map[t] : t;
+  // without a cache (queries alone) only the map's sign marks padding
+  if (slot < 0 || (p.k && slot >= (int64_t)p.num_pages * p.page_size)) return;
+  int64_t page = 0, in_page = 0;
+  if (p.k) {
+    page = (uint32_t)slot / (uint32_t)p.page_size;      // slots are below 2^31
+    in_page = slot - page * p.page_size;
+  }
+  struct Row { int kind, h; };             // 0: q, 1: k, 2: v
+  auto row_of = [&](int r) {
+    return r < Hq ? Row{0, r} : (r < Hq + Hkv ? Row{1, r - Hq} : Row{2, r - Hq - Hkv});
+  };
+  auto source = [&](const Row& w) {
+    const Tx* src = w.kind == 0 ? static_cast<const Tx*>(p.q) + t * p.q_row_stride
+                  : w.kind == 1 ? static_cast<const Tx*>(p.k) + t * p.k_row_stride
+                                : static_cast<const Tx*>(p.v) + t * p.v_row_stride;
+    return src + (int64_t)w.h * D + l * 8;
+  };
+  Raw8<Tx> raw[U];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPW + sub;
+      if (r < end) raw[u].load(source(row_of(r)));
+      else raw[u].zero();
+    }
+  };
+  load(first);
+
+  // (cos, sin) of this lane's dims: 8 in the half layout, 4 pairs in the other
   const int half = p.rope_dims >> 1;
-  for (int i = tid; i < tok * half; i += kThreads) {
-    const int tt = i / half, j = i % half;
-    const int64_t t = t0 + tt;
-    if (t < p.T)
-      cs[i] = turn(p.inv_freq[j], p.positions[(int64_t)(j % p.axes) * p.T + t], p.rope_scale);
-  }
-  if (tid < tok) {
-    const int64_t t = t0 + tid;
-    int64_t slot = -1;
-    if (t < p.T) slot = p.slot_map ? p.slot_map[t] : t;
-    const bool ok = slot >= 0 && slot < (int64_t)p.num_pages * p.page_size;
-    // without a cache (queries alone) only the map's sign marks padding
-    const bool live = t < p.T && (p.k ? ok : slot >= 0);
-    live_at[tid] = live;
-    if (live && p.k) {
-      const int64_t page = slot / p.page_size, off = slot % p.page_size;
-      k_at[tid] = page * p.ks.page + off * p.ks.token;
-      v_at[tid] = page * p.vs.page + off * p.vs.token;
+  float2 cs[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = make_float2(1.f, 0.f);
+  if (l * 8 < p.rope_dims) {
+    const int pos0 = p.positions[t];
+    const int pos1 = p.axes == 3 ? p.positions[p.T + t] : pos0;
+    const int pos2 = p.axes == 3 ? p.positions[2 * p.T + t] : pos0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int d = l * 8 + i;
+      if (p.interleaved ? i < 4 && l * 4 + i < half : d < p.rope_dims) {
+        const int pair = p.interleaved ? l * 4 + i : (d < half ? d : d - half);
+        const int axis = pair % 3;
+        cs[i] = turn(p.inv_freq[pair], axis == 0 ? pos0 : (axis == 1 ? pos1 : pos2),
+                     p.rope_scale);
+        // the half layout adds the partner's sine with the side's sign
+        if (!p.interleaved && d < half) cs[i].y = -cs[i].y;
+      }
     }
   }
-  __syncthreads();
-  const int Hq = p.q ? p.Hq : 0, Hkv = p.k ? p.Hkv : 0;
-  const int H = Hq + 2 * Hkv, rows = tok * H;
+
+  float w[8];
+  int w_kind = -1;
   float* row = stage[warp] + sub * D;
-  for (int r0 = warp * RPW; r0 < rows; r0 += kWarps * RPW) {
-    const int r = r0 + sub;
-    const int tt = min(r, rows - 1) / H, hh = min(r, rows - 1) % H;
-    const int64_t t = t0 + tt;
-    const bool live = r < rows && live_at[tt];
-    const int kind = hh < Hq ? 0 : (hh < Hq + Hkv ? 1 : 2);     // q, k, v
-    const int h = kind == 0 ? hh : (kind == 1 ? hh - Hq : hh - Hq - Hkv);
-    const Tx* src = kind == 0 ? static_cast<const Tx*>(p.q) + t * p.q_row_stride
-                  : kind == 1 ? static_cast<const Tx*>(p.k) + t * p.k_row_stride
-                              : static_cast<const Tx*>(p.v) + t * p.v_row_stride;
-    Raw8<Tx> raw;
-    raw.zero();
-    if (live) raw.load(src + (int64_t)h * D + l * 8);
-    float x[8];
-    raw.to_f32(x);
-    const void* w = kind == 0 ? p.q_norm_w : p.k_norm_w;
-    float ss = 0.f;
+  for (int r0 = first; r0 < end; r0 += U * RPW) {
+    Raw8<Tx> now[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+    for (int u = 0; u < U; ++u) now[u] = raw[u];
+    if (r0 + U * RPW < end) load(r0 + U * RPW);
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (kind != 2 && w) {
-      const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPW + sub;
+      if (r0 + u * RPW >= end) break;              // the same for the warp
+      const bool live = r < end;
+      const Row at = row_of(min(r, end - 1));
+      float x[8];
+      now[u].to_f32(x);
+      const void* weight = at.kind == 0 ? p.q_norm_w : p.k_norm_w;
+      if (at.kind != w_kind && at.kind != 2) {
+        w_kind = at.kind;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * to_f32(w, p.w_dtype, l * 8 + i);
-    }
-    if (half) {
-      if (p.interleaved) {
+        for (int i = 0; i < 8; ++i) w[i] = weight ? to_f32(weight, p.w_dtype, l * 8 + i) : 1.f;
+      }
+      float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const int d = l * 8 + i;
-          if (kind != 2 && live && d < p.rope_dims) {
-            const float2 a = cs[tt * half + (d >> 1)];
-            const float u = x[i], v = x[i + 1];
-            x[i] = u * a.x - v * a.y;
-            x[i + 1] = v * a.x + u * a.y;
-          }
-        }
-      } else {
-        __syncwarp();
+      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row[l * 8 + i] = x[i];
-        __syncwarp();
-        if (kind != 2 && live) {
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (at.kind != 2 && weight) {
+        const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int d = l * 8 + i;
-            if (d < half) {
-              const float2 a = cs[tt * half + d];
-              x[i] = x[i] * a.x - row[d + half] * a.y;
-            } else if (d < p.rope_dims) {
-              const float2 a = cs[tt * half + d - half];
-              x[i] = x[i] * a.x + row[d - half] * a.y;
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+      }
+      if (half) {
+        if (p.interleaved) {
+          if (at.kind != 2 && l * 8 < p.rope_dims) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = x[2 * i], b = x[2 * i + 1];
+              x[2 * i] = a * cs[i].x - b * cs[i].y;
+              x[2 * i + 1] = b * cs[i].x + a * cs[i].y;
             }
+          }
+        } else {
+          // the partner of dim d is d + half or d - half: with half a multiple of
+          // 8 the same element of another lane, else through shared memory
+          float other[8];
+          if (half % 8 == 0) {
+            const int from = sub * LPR + (l * 8 < half ? l + half / 8 : l - half / 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(0xffffffffu, x[i], from & 31);
+          } else {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[l * 8 + i] = x[i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int d = l * 8 + i;
+              other[i] = d < p.rope_dims ? row[d < half ? d + half : d - half] : 0.f;
+            }
+          }
+          if (at.kind != 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (l * 8 + i < p.rope_dims) x[i] = x[i] * cs[i].x + other[i] * cs[i].y;
           }
         }
       }
+      if (!live) continue;
+      To* dst = at.kind == 0 ? static_cast<To*>(p.q_out) + (t * p.Hq + at.h) * D
+              : at.kind == 1
+                  ? static_cast<To*>(p.k_cache) + page * p.ks.page + in_page * p.ks.token +
+                        at.h * p.ks.head
+                  : static_cast<To*>(p.v_cache) + page * p.vs.page + in_page * p.vs.token +
+                        at.h * p.vs.head;
+      put8(dst + l * 8, x);
     }
-    if (!live) continue;
-    To* dst = kind == 0 ? static_cast<To*>(p.q_out) + (t * p.Hq + h) * D
-            : kind == 1 ? static_cast<To*>(p.k_cache) + k_at[tt] + h * p.ks.head
-                        : static_cast<To*>(p.v_cache) + v_at[tt] + h * p.vs.head;
-    put8(dst + l * 8, x);
   }
 }
 
@@ -177,10 +224,23 @@ __global__ void rope_inv_freq_kernel(int pairs, double log2_base, double factor,
 }
 
 template <class Tx, class To>
-cudaError_t launch_typed(const NormRopeArgs& a, unsigned grid, int tok, size_t smem) {
-  if (a.D == 256) qk_norm_rope_kernel<Tx, To, 256><<<grid, kThreads, smem, a.stream>>>(a, tok);
-  else if (a.D == 128) qk_norm_rope_kernel<Tx, To, 128><<<grid, kThreads, smem, a.stream>>>(a, tok);
-  else qk_norm_rope_kernel<Tx, To, 64><<<grid, kThreads, smem, a.stream>>>(a, tok);
+cudaError_t launch_typed(const NormRopeArgs& a) {
+  const int H = (a.q ? a.Hq : 0) + 2 * (a.k ? a.Hkv : 0);
+  const int rpw = 32 / (a.D / 8);          // rows per warp and pass
+  const int passes = (H + rpw - 1) / rpw;
+  // shares of a token's heads until there are warps for every SM, a pass at least
+  int64_t shares = (148 * 16 + a.T - 1) / a.T;
+  if (shares > passes) shares = passes;
+  const int share_rows = (int)((passes + shares - 1) / shares) * rpw;
+  shares = (H + share_rows - 1) / share_rows;
+  const unsigned grid = (unsigned)((a.T * shares + kWarps - 1) / kWarps);
+  const int s = (int)shares;
+  if (a.D == 256)
+    qk_norm_rope_kernel<Tx, To, 256><<<grid, kThreads, 0, a.stream>>>(a, s, share_rows);
+  else if (a.D == 128)
+    qk_norm_rope_kernel<Tx, To, 128><<<grid, kThreads, 0, a.stream>>>(a, s, share_rows);
+  else
+    qk_norm_rope_kernel<Tx, To, 64><<<grid, kThreads, 0, a.stream>>>(a, s, share_rows);
   return cudaGetLastError();
 }
 
@@ -188,18 +248,13 @@ cudaError_t launch_typed(const NormRopeArgs& a, unsigned grid, int tok, size_t s
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a) {
   if (a.T == 0) return cudaSuccess;
-  const int tok = a.T > 4 * 148 ? kMaxTok : 1;
-  const unsigned grid = (unsigned)((a.T + tok - 1) / tok);
-  const size_t smem = (size_t)tok * (a.rope_dims / 2) * sizeof(float2);
   const bool h = a.out_dtype == GDN_F16;
-  if (a.x_dtype == GDN_F32)
-    return h ? launch_typed<float, __half>(a, grid, tok, smem)
-             : launch_typed<float, __nv_bfloat16>(a, grid, tok, smem);
-  if (a.x_dtype == GDN_F16)
-    return h ? launch_typed<__half, __half>(a, grid, tok, smem)
-             : launch_typed<__half, __nv_bfloat16>(a, grid, tok, smem);
-  return h ? launch_typed<__nv_bfloat16, __half>(a, grid, tok, smem)
-           : launch_typed<__nv_bfloat16, __nv_bfloat16>(a, grid, tok, smem);
+  if (a.x_dtype == GDN_F32) return h ? launch_typed<float, __half>(a)
+                                     : launch_typed<float, __nv_bfloat16>(a);
+  if (a.x_dtype == GDN_F16) return h ? launch_typed<__half, __half>(a)
+                                     : launch_typed<__half, __nv_bfloat16>(a);
+  return h ? launch_typed<__nv_bfloat16, __half>(a)
+           : launch_typed<__nv_bfloat16, __nv_bfloat16>(a);
 }
 
 cudaError_t launch_rope_inv_freq(int rope_dims, double base, double factor, double context,
