@@ -33,19 +33,23 @@ __device__ __forceinline__ float to_f32(const void* w, gdn_dtype t, int i) {
   return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
 
-// Round to nearest; finite values past the type's range become its largest,
-// NaN stays NaN.
-__device__ __forceinline__ float clamp_h(float x) {
-  return x != x ? x : fminf(fmaxf(x, -65504.f), 65504.f);
-}
-__device__ __forceinline__ void put8(__half* p, const float (&f)[8]) {
+// Round to nearest; values past the type's range become its largest, NaN stays
+// NaN.
+__device__ __forceinline__ void put8(__half* p, const float2 (&f)[4]) {
   uint4 u;
-  __half2* h = reinterpret_cast<__half2*>(&u);
+  uint32_t* h = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(clamp_h(f[2 * i]), clamp_h(f[2 * i + 1]));
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(f[i].y), "f"(f[i].x));
   *reinterpret_cast<uint4*>(p) = u;
 }
-__device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&f)[8]) { store8(p, f); }
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const float2 (&f)[4]) {
+  uint4 u;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[i].x, f[i].y);
+  *reinterpret_cast<uint4*>(p) = u;
+}
 
 __device__ __forceinline__ float2 turn(double inv_freq, int pos, float scale) {
   double f = inv_freq * 0.15915494309189533577;         // 1 / (2 pi)
@@ -58,20 +62,160 @@ __device__ __forceinline__ float2 turn(double inv_freq, int pos, float scale) {
   return make_float2(c * scale, s * scale);
 }
 
+// What a lane keeps for its token: (cos, sin) of its dims, 8 in the half layout
+// (the sine with its side's sign), 4 pairs in the other.
+struct Turns { float2 cs[8]; };
+
+// Heads h0 .. h1-1 of one kind (0: q, 1: k, 2: v) of the token by a warp.
+template <int KIND, class Tx, class To, int D>
+__device__ __forceinline__ void do_heads(const NormRopeArgs& p, const Tx* src, To* dst,
+                                         int64_t dst_head, int h0, int h1, const Turns& turns,
+                                         float* stage, int lane) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr int U = 2;                     // passes in flight
+  const int sub = lane / LPR, l = lane % LPR;
+  const int half = p.rope_dims >> 1;
+  const bool turned = KIND != 2 && l * 8 < p.rope_dims;
+  const int from = sub * LPR + (l * 8 < half ? l + half / 8 : l - half / 8);
+  const void* weight = KIND == 0 ? p.q_norm_w : p.k_norm_w;
+  src += l * 8;
+  dst += l * 8;
+  Raw8<Tx> raw[U];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (h + u * RPW + sub < h1) raw[u].load(src + (int64_t)(h + u * RPW + sub) * D);
+      else raw[u].zero();
+    }
+  };
+  load(h0);
+  float2 w[4];
+  if (KIND != 2 && weight) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = make_float2(to_f32(weight, p.w_dtype, l * 8 + 2 * i),
+                         to_f32(weight, p.w_dtype, l * 8 + 2 * i + 1));
+  }
+  for (int h = h0; h < h1; h += U * RPW) {
+    float2 x[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[8];
+      raw[u].to_f32(f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[u][i] = make_float2(f[2 * i], f[2 * i + 1]);
+    }
+    if (h + U * RPW < h1) load(h + U * RPW);
+    if (KIND != 2 && weight) {
+      float ss[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float2 t = __fmul2_rn(x[u][0], x[u][0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) t = __ffma2_rn(x[u][i], x[u][i], t);
+        ss[u] = t.x + t.y;
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float inv = rsqrtf(ss[u] * (1.0f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[u][i] = __fmul2_rn(__fmul2_rn(x[u][i], make_float2(inv, inv)), w[i]);
+      }
+    }
+    if (KIND != 2 && half) {
+      if (p.interleaved) {
+        if (turned) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 c = turns.cs[i], v = x[u][i];
+              x[u][i] = make_float2(v.x * c.x - v.y * c.y, v.y * c.x + v.x * c.y);
+            }
+        }
+      } else {
+        // the partner of dim d is d + half or d - half: with half a multiple of 8
+        // the same element of another lane, else through shared memory
+        float2 other[U][4];
+        if (half % 8 == 0) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              other[u][i] = make_float2(__shfl_sync(0xffffffffu, x[u][i].x, from & 31),
+                                        __shfl_sync(0xffffffffu, x[u][i].y, from & 31));
+        } else {
+          float* row = stage + sub * D;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(row + l * 8 + 2 * i) = x[u][i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int d = l * 8 + 2 * i;
+              other[u][i].x = d < p.rope_dims ? row[d < half ? d + half : d - half] : 0.f;
+              other[u][i].y =
+                  d + 1 < p.rope_dims ? row[d + 1 < half ? d + 1 + half : d + 1 - half] : 0.f;
+            }
+          }
+        }
+        if (turned) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 a = turns.cs[2 * i], b = turns.cs[2 * i + 1];
+              x[u][i] = __ffma2_rn(other[u][i], make_float2(a.y, b.y),
+                                   __fmul2_rn(x[u][i], make_float2(a.x, b.x)));
+            }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = h + u * RPW + sub;
+      if (at < h1) put8(dst + at * dst_head, x[u]);
+    }
+  }
+}
+
 template <class Tx, class To, int D>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeArgs p, int shares,
-                                                                int share_rows) {
+                                                                int share_passes) {
   constexpr int LPR = D / 8;               // lanes per row
   constexpr int RPW = 32 / LPR;            // rows per warp and pass
-  constexpr int U = sizeof(Tx) == 4 ? 2 : 4;       // passes in flight
-  __shared__ float stage[kWarps][256];     // rows being turned, see below
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane / LPR, l = lane % LPR;
+  __shared__ __align__(8) float stage[kWarps][256];     // angles, then rows being turned
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPR;
   const int64_t task = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t t = task / shares;
   if (t >= p.T) return;
-  const int Hq = p.q ? p.Hq : 0, Hkv = p.k ? p.Hkv : 0, H = Hq + 2 * Hkv;
-  const int first = (int)(task - t * shares) * share_rows, end = min(first + share_rows, H);
+  const int Hq = p.q ? p.Hq : 0, Hkv = p.k ? p.Hkv : 0;
+  // passes of RPW heads: first those of q, then k, then v
+  const int pq = (Hq + RPW - 1) / RPW, pkv = (Hkv + RPW - 1) / RPW;
+  const int a = (int)(task - t * shares) * share_passes, b = a + share_passes;
+  const int q0 = a * RPW, q1 = min(b * RPW, Hq);
+  const int k0 = max(a - pq, 0) * RPW, k1 = min((b - pq) * RPW, Hkv);
+  const int v0 = max(a - pq - pkv, 0) * RPW, v1 = min((b - pq - pkv) * RPW, Hkv);
+  const Tx* q = static_cast<const Tx*>(p.q) + t * p.q_row_stride;
+  const Tx* k = static_cast<const Tx*>(p.k) + t * p.k_row_stride;
+  const Tx* v = static_cast<const Tx*>(p.v) + t * p.v_row_stride;
+  // the whole share is on its way while the angles are made
+  auto prefetch = [&](const Tx* x, int h0, int h1) {
+    const char* at = reinterpret_cast<const char*>(x + (int64_t)h0 * D);
+    const int bytes = (h1 - h0) * D * (int)sizeof(Tx);
+    for (int i = lane * 128; i < bytes; i += 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+  };
+  prefetch(q, q0, q1);
+  prefetch(k, k0, k1);
+  prefetch(v, v0, v1);
 
   const int64_t slot = p.slot_map ? p.slot_map[t] : t;
   // without a cache (queries alone) only the map's sign marks padding
@@ -81,128 +225,46 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeAr
     page = (uint32_t)slot / (uint32_t)p.page_size;      // slots are below 2^31
     in_page = slot - page * p.page_size;
   }
-  struct Row { int kind, h; };             // 0: q, 1: k, 2: v
-  auto row_of = [&](int r) {
-    return r < Hq ? Row{0, r} : (r < Hq + Hkv ? Row{1, r - Hq} : Row{2, r - Hq - Hkv});
-  };
-  auto source = [&](const Row& w) {
-    const Tx* src = w.kind == 0 ? static_cast<const Tx*>(p.q) + t * p.q_row_stride
-                  : w.kind == 1 ? static_cast<const Tx*>(p.k) + t * p.k_row_stride
-                                : static_cast<const Tx*>(p.v) + t * p.v_row_stride;
-    return src + (int64_t)w.h * D + l * 8;
-  };
-  Raw8<Tx> raw[U];
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * RPW + sub;
-      if (r < end) raw[u].load(source(row_of(r)));
-      else raw[u].zero();
-    }
-  };
-  load(first);
 
-  // (cos, sin) of this lane's dims: 8 in the half layout, 4 pairs in the other
   const int half = p.rope_dims >> 1;
-  float2 cs[8];
+  Turns turns;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = make_float2(1.f, 0.f);
-  if (l * 8 < p.rope_dims) {
+  for (int i = 0; i < 8; ++i) turns.cs[i] = make_float2(1.f, 0.f);
+  if (half) {
+    // each angle once per warp, a pair per lane and turn
+    float2* cs = reinterpret_cast<float2*>(stage[warp]);
     const int pos0 = p.positions[t];
     const int pos1 = p.axes == 3 ? p.positions[p.T + t] : pos0;
     const int pos2 = p.axes == 3 ? p.positions[2 * p.T + t] : pos0;
+    for (int j = lane; j < half; j += 32) {
+      const int axis = j % 3;
+      cs[j] = turn(p.inv_freq[j], axis == 0 ? pos0 : (axis == 1 ? pos1 : pos2), p.rope_scale);
+    }
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int d = l * 8 + i;
-      if (p.interleaved ? i < 4 && l * 4 + i < half : d < p.rope_dims) {
-        const int pair = p.interleaved ? l * 4 + i : (d < half ? d : d - half);
-        const int axis = pair % 3;
-        cs[i] = turn(p.inv_freq[pair], axis == 0 ? pos0 : (axis == 1 ? pos1 : pos2),
-                     p.rope_scale);
-        // the half layout adds the partner's sine with the side's sign
-        if (!p.interleaved && d < half) cs[i].y = -cs[i].y;
+      if (p.interleaved) {
+        if (i < 4 && l * 4 + i < half) turns.cs[i] = cs[l * 4 + i];
+      } else if (d < p.rope_dims) {
+        turns.cs[i] = cs[d < half ? d : d - half];
+        if (d < half) turns.cs[i].y = -turns.cs[i].y;
       }
     }
+    __syncwarp();
   }
 
-  float w[8];
-  int w_kind = -1;
-  float* row = stage[warp] + sub * D;
-  for (int r0 = first; r0 < end; r0 += U * RPW) {
-    Raw8<Tx> now[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) now[u] = raw[u];
-    if (r0 + U * RPW < end) load(r0 + U * RPW);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * RPW + sub;
-      if (r0 + u * RPW >= end) break;              // the same for the warp
-      const bool live = r < end;
-      const Row at = row_of(min(r, end - 1));
-      float x[8];
-      now[u].to_f32(x);
-      const void* weight = at.kind == 0 ? p.q_norm_w : p.k_norm_w;
-      if (at.kind != w_kind && at.kind != 2) {
-        w_kind = at.kind;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = weight ? to_f32(weight, p.w_dtype, l * 8 + i) : 1.f;
-      }
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (at.kind != 2 && weight) {
-        const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
-      }
-      if (half) {
-        if (p.interleaved) {
-          if (at.kind != 2 && l * 8 < p.rope_dims) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = x[2 * i], b = x[2 * i + 1];
-              x[2 * i] = a * cs[i].x - b * cs[i].y;
-              x[2 * i + 1] = b * cs[i].x + a * cs[i].y;
-            }
-          }
-        } else {
-          // the partner of dim d is d + half or d - half: with half a multiple of
-          // 8 the same element of another lane, else through shared memory
-          float other[8];
-          if (half % 8 == 0) {
-            const int from = sub * LPR + (l * 8 < half ? l + half / 8 : l - half / 8);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(0xffffffffu, x[i], from & 31);
-          } else {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) row[l * 8 + i] = x[i];
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int d = l * 8 + i;
-              other[i] = d < p.rope_dims ? row[d < half ? d + half : d - half] : 0.f;
-            }
-          }
-          if (at.kind != 2) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (l * 8 + i < p.rope_dims) x[i] = x[i] * cs[i].x + other[i] * cs[i].y;
-          }
-        }
-      }
-      if (!live) continue;
-      To* dst = at.kind == 0 ? static_cast<To*>(p.q_out) + (t * p.Hq + at.h) * D
-              : at.kind == 1
-                  ? static_cast<To*>(p.k_cache) + page * p.ks.page + in_page * p.ks.token +
-                        at.h * p.ks.head
-                  : static_cast<To*>(p.v_cache) + page * p.vs.page + in_page * p.vs.token +
-                        at.h * p.vs.head;
-      put8(dst + l * 8, x);
-    }
-  }
+  if (q0 < q1)
+    do_heads<0, Tx, To, D>(p, q, static_cast<To*>(p.q_out) + t * p.Hq * D, D, q0, q1, turns,
+                           stage[warp], lane);
+  if (k0 < k1)
+    do_heads<1, Tx, To, D>(p, k,
+                           static_cast<To*>(p.k_cache) + page * p.ks.page + in_page * p.ks.token,
+                           p.ks.head, k0, k1, turns, stage[warp], lane);
+  if (v0 < v1)
+    do_heads<2, Tx, To, D>(p, v,
+                           static_cast<To*>(p.v_cache) + page * p.vs.page + in_page * p.vs.token,
+                           p.vs.head, v0, v1, turns, stage[warp], lane);
 }
 
 // Rotary frequencies: f_i = base^(-2i / R). With factor > 1 either all are
@@ -225,22 +287,21 @@ __global__ void rope_inv_freq_kernel(int pairs, double log2_base, double factor,
 
 template <class Tx, class To>
 cudaError_t launch_typed(const NormRopeArgs& a) {
-  const int H = (a.q ? a.Hq : 0) + 2 * (a.k ? a.Hkv : 0);
   const int rpw = 32 / (a.D / 8);          // rows per warp and pass
-  const int passes = (H + rpw - 1) / rpw;
+  const int passes = ((a.q ? a.Hq : 0) + rpw - 1) / rpw + 2 * (((a.k ? a.Hkv : 0) + rpw - 1) / rpw);
   // shares of a token's heads until there are warps for every SM, a pass at least
   int64_t shares = (148 * 16 + a.T - 1) / a.T;
   if (shares > passes) shares = passes;
-  const int share_rows = (int)((passes + shares - 1) / shares) * rpw;
-  shares = (H + share_rows - 1) / share_rows;
+  const int share_passes = (int)((passes + shares - 1) / shares);
+  shares = (passes + share_passes - 1) / share_passes;
   const unsigned grid = (unsigned)((a.T * shares + kWarps - 1) / kWarps);
   const int s = (int)shares;
   if (a.D == 256)
-    qk_norm_rope_kernel<Tx, To, 256><<<grid, kThreads, 0, a.stream>>>(a, s, share_rows);
+    qk_norm_rope_kernel<Tx, To, 256><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
   else if (a.D == 128)
-    qk_norm_rope_kernel<Tx, To, 128><<<grid, kThreads, 0, a.stream>>>(a, s, share_rows);
+    qk_norm_rope_kernel<Tx, To, 128><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
   else
-    qk_norm_rope_kernel<Tx, To, 64><<<grid, kThreads, 0, a.stream>>>(a, s, share_rows);
+    qk_norm_rope_kernel<Tx, To, 64><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
   return cudaGetLastError();
 }
 
