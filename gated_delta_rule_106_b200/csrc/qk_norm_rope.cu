@@ -24,7 +24,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
 constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ float to_f32(const void* w, gdn_dtype t, int i) {
@@ -62,12 +62,19 @@ __device__ __forceinline__ float2 turn(double inv_freq, int pos, float scale) {
   return make_float2(c * scale, s * scale);
 }
 
+// How a lane finds the partner of dim d, which decides the registers it needs
+// (one kernel for all held 123 and reached 5.2 TB/s at 32768 tokens; 96 without
+// the staged exchange and 5.6): adjacent pairs are its own; in the half layout
+// the partner is d +- R / 2, the same element of another lane where R / 2 is a
+// multiple of 8, else through shared memory.
+enum Partner { kOwn, kLane, kStaged };
+
 // What a lane keeps for its token: (cos, sin) of its dims, 8 in the half layout
 // (the sine with its side's sign), 4 pairs in the other.
 struct Turns { float2 cs[8]; };
 
 // Heads h0 .. h1-1 of one kind (0: q, 1: k, 2: v) of the token by a warp.
-template <int KIND, class Tx, class To, int D>
+template <int KIND, Partner PARTNER, class Tx, class To, int D>
 __device__ __forceinline__ void do_heads(const NormRopeArgs& p, const Tx* src, To* dst,
                                          int64_t dst_head, int h0, int h1, const Turns& turns,
                                          float* stage, int lane) {
@@ -128,7 +135,7 @@ __device__ __forceinline__ void do_heads(const NormRopeArgs& p, const Tx* src, T
       }
     }
     if (KIND != 2 && half) {
-      if (p.interleaved) {
+      if constexpr (PARTNER == kOwn) {
         if (turned) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -139,10 +146,8 @@ __device__ __forceinline__ void do_heads(const NormRopeArgs& p, const Tx* src, T
             }
         }
       } else {
-        // the partner of dim d is d + half or d - half: with half a multiple of 8
-        // the same element of another lane, else through shared memory
         float2 other[U][4];
-        if (half % 8 == 0) {
+        if constexpr (PARTNER == kLane) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -186,7 +191,7 @@ __device__ __forceinline__ void do_heads(const NormRopeArgs& p, const Tx* src, T
   }
 }
 
-template <class Tx, class To, int D>
+template <Partner PARTNER, class Tx, class To, int D>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeArgs p, int shares,
                                                                 int share_passes) {
   constexpr int LPR = D / 8;               // lanes per row
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeAr
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int d = l * 8 + i;
-      if (p.interleaved) {
+      if constexpr (PARTNER == kOwn) {
         if (i < 4 && l * 4 + i < half) turns.cs[i] = cs[l * 4 + i];
       } else if (d < p.rope_dims) {
         turns.cs[i] = cs[d < half ? d : d - half];
@@ -255,14 +260,14 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeAr
   }
 
   if (q0 < q1)
-    do_heads<0, Tx, To, D>(p, q, static_cast<To*>(p.q_out) + t * p.Hq * D, D, q0, q1, turns,
+    do_heads<0, PARTNER, Tx, To, D>(p, q, static_cast<To*>(p.q_out) + t * p.Hq * D, D, q0, q1, turns,
                            stage[warp], lane);
   if (k0 < k1)
-    do_heads<1, Tx, To, D>(p, k,
+    do_heads<1, PARTNER, Tx, To, D>(p, k,
                            static_cast<To*>(p.k_cache) + page * p.ks.page + in_page * p.ks.token,
                            p.ks.head, k0, k1, turns, stage[warp], lane);
   if (v0 < v1)
-    do_heads<2, Tx, To, D>(p, v,
+    do_heads<2, PARTNER, Tx, To, D>(p, v,
                            static_cast<To*>(p.v_cache) + page * p.vs.page + in_page * p.vs.token,
                            p.vs.head, v0, v1, turns, stage[warp], lane);
 }
@@ -285,7 +290,7 @@ __global__ void rope_inv_freq_kernel(int pairs, double log2_base, double factor,
   out[i] = f * (keep + (1.0 - keep) / factor);
 }
 
-template <class Tx, class To>
+template <Partner PARTNER, class Tx, class To>
 cudaError_t launch_typed(const NormRopeArgs& a) {
   const int rpw = 32 / (a.D / 8);          // rows per warp and pass
   const int passes = ((a.q ? a.Hq : 0) + rpw - 1) / rpw + 2 * (((a.k ? a.Hkv : 0) + rpw - 1) / rpw);
@@ -297,25 +302,31 @@ cudaError_t launch_typed(const NormRopeArgs& a) {
   const unsigned grid = (unsigned)((a.T * shares + kWarps - 1) / kWarps);
   const int s = (int)shares;
   if (a.D == 256)
-    qk_norm_rope_kernel<Tx, To, 256><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
+    qk_norm_rope_kernel<PARTNER, Tx, To, 256><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
   else if (a.D == 128)
-    qk_norm_rope_kernel<Tx, To, 128><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
+    qk_norm_rope_kernel<PARTNER, Tx, To, 128><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
   else
-    qk_norm_rope_kernel<Tx, To, 64><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
+    qk_norm_rope_kernel<PARTNER, Tx, To, 64><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
   return cudaGetLastError();
+}
+
+template <class Tx, class To>
+cudaError_t launch_layout(const NormRopeArgs& a) {
+  if (a.interleaved || a.rope_dims == 0) return launch_typed<kOwn, Tx, To>(a);
+  return a.rope_dims % 16 == 0 ? launch_typed<kLane, Tx, To>(a) : launch_typed<kStaged, Tx, To>(a);
+}
+template <class Tx>
+cudaError_t launch_out(const NormRopeArgs& a) {
+  return a.out_dtype == GDN_F16 ? launch_layout<Tx, __half>(a)
+                                : launch_layout<Tx, __nv_bfloat16>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a) {
   if (a.T == 0) return cudaSuccess;
-  const bool h = a.out_dtype == GDN_F16;
-  if (a.x_dtype == GDN_F32) return h ? launch_typed<float, __half>(a)
-                                     : launch_typed<float, __nv_bfloat16>(a);
-  if (a.x_dtype == GDN_F16) return h ? launch_typed<__half, __half>(a)
-                                     : launch_typed<__half, __nv_bfloat16>(a);
-  return h ? launch_typed<__nv_bfloat16, __half>(a)
-           : launch_typed<__nv_bfloat16, __nv_bfloat16>(a);
+  if (a.x_dtype == GDN_F32) return launch_out<float>(a);
+  return a.x_dtype == GDN_F16 ? launch_out<__half>(a) : launch_out<__nv_bfloat16>(a);
 }
 
 cudaError_t launch_rope_inv_freq(int rope_dims, double base, double factor, double context,
