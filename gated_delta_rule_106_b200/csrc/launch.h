@@ -99,6 +99,26 @@ struct AttnDecodeArgs {
   cudaStream_t stream;
 };
 
+// n / d for 0 <= n < 2^31 by one wide multiplication: with 2^(s-1) < d <= 2^s and
+// m = floor(2^(31+s) / d) + 1, m d exceeds 2^(31+s) by at most 2^s, so
+// floor(n m / 2^(31+s)) = floor(n / d) for such n.
+struct FastDiv {
+  uint32_t m;
+  int s;
+  explicit FastDiv(int d) {
+    s = 0;
+    while (s < 31 && (1u << s) < (uint32_t)d) ++s;
+    m = (uint32_t)(((uint64_t)1 << (31 + s)) / (uint32_t)d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s));
+  }
+  // ceil(n / d)
+  __device__ __forceinline__ int up(int n) const { return n > 0 ? (*this)(n - 1) + 1 : 0; }
+#endif
+};
+
 // Page plan: block tables, free stack, slots and positions from request lengths.
 constexpr int kPlanMaxRequests = 16384;   // running sums of 3 x 4 bytes each in shared memory
 struct PagePlanArgs {

@@ -23,17 +23,16 @@
 namespace gdn {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kMaxThreads = 1024;
+constexpr int kKeep = 4;          // requests a thread keeps in registers
 
 struct Sums { uint32_t tok, take, back; };
 
 struct PlanShared {
-  Sums warp[kPlanThreads / 32];
+  Sums warp[kMaxThreads / 32];
   Sums total, grant;      // grant: sums over the granted requests
   uint32_t refused;
 };
-
-__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
 // Saturating running sums: past the limits only "does not fit" is of interest.
 struct Limits { uint32_t tok, take; };
@@ -55,44 +54,70 @@ __device__ __forceinline__ int last_le(const uint32_t* a, int n, uint32_t x) {
   return lo;
 }
 
-struct Request { int len, want; bool grow, shrink; };
-__device__ __forceinline__ Request request(const PagePlanArgs& p, int n) {
-  Request r{p.lens[n], p.want[n], false, false};
-  const int64_t cap = (int64_t)p.max_pages * p.page_size;
-  const bool fine = r.len >= 0 && r.want >= 0 && r.len <= cap && r.want <= cap;
-  r.grow = fine && r.want > r.len;
-  r.shrink = fine && r.want < r.len;
+struct PlanParams {
+  PagePlanArgs a;
+  FastDiv page;
+};
+
+// A request: its lengths, and what it asks of the running sums.
+struct Request {
+  int len, want;
+  Sums s;
+  __device__ bool grow() const { return s.tok != 0; }
+  __device__ bool shrink() const { return valid && want < len; }
+  bool valid;
+};
+__device__ __forceinline__ Request request(const PlanParams& p, int n, const Limits& lim) {
+  Request r{p.a.lens[n], p.a.want[n], Sums{0u, 0u, 0u}, false};
+  const int64_t cap = (int64_t)p.a.max_pages * p.a.page_size;
+  r.valid = r.len >= 0 && r.want >= 0 && r.len <= cap && r.want <= cap;
+  if (r.valid) {
+    const int pages = p.page.up(r.want) - p.page.up(r.len);
+    if (r.want > r.len) {
+      r.s.tok = min((uint32_t)(r.want - r.len), lim.tok);
+      r.s.take = min((uint32_t)pages, lim.take);
+    } else {
+      r.s.back = (uint32_t)-pages;
+    }
+  }
   return r;
 }
-__device__ __forceinline__ Sums demand(const PagePlanArgs& p, const Request& r,
-                                       const Limits& lim) {
-  Sums s{0u, 0u, 0u};
-  if (r.grow) {
-    s.tok = min((uint32_t)(r.want - r.len), lim.tok);
-    s.take = min((uint32_t)(ceil_div(r.want, p.page_size) - ceil_div(r.len, p.page_size)),
-                 lim.take);
-  } else if (r.shrink) {
-    s.back = (uint32_t)(ceil_div(r.len, p.page_size) - ceil_div(r.want, p.page_size));
-  }
-  return s;
-}
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanArgs p) {
+// KEEP: at most kKeep requests per thread, read once and kept.
+template <bool KEEP>
+__global__ void __launch_bounds__(kMaxThreads) page_plan_kernel(const PlanParams pp) {
   extern __shared__ uint32_t sums[];            // cu | take | back, N + 1 each
   __shared__ PlanShared sh;
+  const PagePlanArgs& p = pp.a;
   uint32_t* cu = sums;
   uint32_t* take = sums + (p.N + 1);
   uint32_t* back = take + (p.N + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const Limits lim{(uint32_t)p.token_capacity + 1u, (uint32_t)p.num_pages + 1u};
   const bool writer = blockIdx.x == 0;
   if (tid == 0) sh.refused = 0;
 
   // running sums: a run of requests per thread, then over the threads
-  const int per = (p.N + kPlanThreads - 1) / kPlanThreads;
+  const int per = (p.N + threads - 1) / threads;
   const int n0 = min(tid * per, p.N), n1 = min(n0 + per, p.N);
+  Request kept[KEEP ? kKeep : 1];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (n0 + i < n1) kept[i] = request(pp, n0 + i, lim);
+  }
+  auto each = [&](auto&& body) {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (n0 + i < n1) body(n0 + i, kept[i]);
+    } else {
+      for (int n = n0; n < n1; ++n) body(n, request(pp, n, lim));
+    }
+  };
+  const uint32_t count = (uint32_t)min(max(p.free_count[0], 0), p.num_pages);
   Sums mine{0u, 0u, 0u};
-  for (int n = n0; n < n1; ++n) mine = add(mine, demand(p, request(p, n), lim), lim);
+  each([&](int, const Request& r) { mine = add(mine, r.s, lim); });
   Sums incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -102,7 +127,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanA
   if (lane == 31) sh.warp[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    Sums w = sh.warp[lane];
+    Sums w = lane < threads / 32 ? sh.warp[lane] : Sums{0u, 0u, 0u};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const Sums v = shfl_up(w, o);
@@ -116,39 +141,37 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanA
   if (lane == 0) run = Sums{0u, 0u, 0u};
   if (warp > 0) run = add(sh.warp[warp - 1], run, lim);
 
-  const uint32_t count = (uint32_t)min(max(p.free_count[0], 0), p.num_pages);
   const uint32_t back_all = min(sh.total.back, (uint32_t)p.num_pages - count);
   const uint32_t avail = count + back_all;      // entries of the stack after the returns
   auto fits = [&](const Sums& s) {
     return s.take <= avail && s.tok <= (uint32_t)p.token_capacity;
   };
   // the request at which "fits" turns false (at most one) gives the granted sums
-  {
+  if (!fits(sh.total)) {
     Sums r = run;
-    for (int n = n0; n < n1; ++n) {
-      const Sums next = add(r, demand(p, request(p, n), lim), lim);
+    each([&](int, const Request& q) {
+      const Sums next = add(r, q.s, lim);
       if (fits(r) && !fits(next)) { sh.grant.tok = r.tok; sh.grant.take = r.take; }
       r = next;
-    }
+    });
+    __syncthreads();
   }
-  __syncthreads();
   const uint32_t tok_all = sh.grant.tok, take_all = sh.grant.take;
   int refused = 0;
-  for (int n = n0; n < n1; ++n) {
-    const Request q = request(p, n);
-    const Sums next = add(run, demand(p, q, lim), lim);
+  each([&](int n, const Request& q) {
+    const Sums next = add(run, q.s, lim);
     const bool before = fits(run);
     cu[n] = before ? run.tok : tok_all;
     take[n] = before ? run.take : take_all;
     back[n] = run.back;
     if (writer) {
-      const bool ok = q.shrink || (q.grow && fits(next));
+      const bool ok = q.shrink() || (q.grow() && fits(next));
       p.new_lens[n] = ok ? q.want : q.len;
       p.cu_new[n] = (int)cu[n];
       refused += q.want != q.len && !ok;
     }
     run = next;
-  }
+  });
   if (refused) atomicAdd(&sh.refused, (uint32_t)refused);
   if (tid == 0) { cu[p.N] = tok_all; take[p.N] = take_all; back[p.N] = sh.total.back; }
   __syncthreads();
@@ -168,13 +191,13 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanA
     if (v < count) return p.free_pages[v];
     const uint32_t w = v - count;
     const int m = last_le(back, p.N, w);
-    const int goal = ceil_div(p.want[m], p.page_size);
+    const int goal = pp.page.up(p.want[m]);
     return p.table[(int64_t)m * p.table_row_stride + goal + (int)(w - back[m])];
   };
-  const uint32_t first = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
+  const uint32_t first = blockIdx.x * threads + tid, step = gridDim.x * threads;
   for (uint32_t i = first; i < take_all; i += step) {
     const int m = last_le(take, p.N, i);
-    const int held = ceil_div(p.lens[m], p.page_size);
+    const int held = pp.page.up(p.lens[m]);
     p.table[(int64_t)m * p.table_row_stride + held + (int)(i - take[m])] = entry(avail - 1 - i);
   }
   for (uint32_t v = count + first; v < avail - take_all; v += step) p.free_pages[v] = entry(v);
@@ -193,9 +216,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanA
         while (t >= cu[m + 1]) ++m;             // ends: cu[N] = tok_all > t
         const int len = p.lens[m];
         pos[e] = len + (int)(t - cu[m]);
-        const int j = pos[e] / p.page_size;
+        const int j = pp.page(pos[e]);
         if (m != last_m || j != last_j) {
-          const int held = ceil_div(len, p.page_size);
+          const int held = pp.page.up(len);
           page = j < held ? p.table[(int64_t)m * p.table_row_stride + j]
                           : entry(avail - 1 - (take[m] + (uint32_t)(j - held)));
           last_m = m;
@@ -222,17 +245,22 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanA
 
 cudaError_t launch_page_plan(const PagePlanArgs& a) {
   const size_t smem = 3 * sizeof(uint32_t) * ((size_t)a.N + 1);
-  if (smem > 48 * 1024) {
+  const PlanParams p{a, FastDiv(a.page_size)};
+  auto kernel = a.N <= kKeep * kMaxThreads ? page_plan_kernel<true> : page_plan_kernel<false>;
+  if (smem > 32 * 1024) {
     // always the largest size, so that concurrent calls do not lower each other's limit
     const cudaError_t e = cudaFuncSetAttribute(
-        page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
         (int)(3 * sizeof(uint32_t) * (kPlanMaxRequests + 1)));
     if (e != cudaSuccess) return e;
   }
+  // threads for a request and four tokens each, in one CTA where that goes; then
   // one CTA per 4096 tokens of the budget, up to one per SM
-  const int64_t want = (a.token_capacity + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  const int64_t work = a.token_capacity / 4 > a.N ? a.token_capacity / 4 : a.N;
+  const int threads = work <= 128 ? 128 : (work <= 512 ? 512 : kMaxThreads);
+  const int64_t want = (a.token_capacity + 4 * threads - 1) / (4 * threads);
   const unsigned grid = (unsigned)(want < 1 ? 1 : (want > 148 ? 148 : want));
-  page_plan_kernel<<<grid, kPlanThreads, smem, a.stream>>>(a);
+  kernel<<<grid, threads, smem, a.stream>>>(p);
   return cudaGetLastError();
 }
 
