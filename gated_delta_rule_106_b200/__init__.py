@@ -1,7 +1,7 @@
 """gated_delta_rule_106_b200 -- B200-native gated delta-rule layer.
 
-Thin ctypes binding over the C ABI of ``libgdn.so`` (declared in
-``include/gdn.h``). Each function here has the name of its C entry point and
+Thin binding (ctypes; a compiled extension for the paged-cache calls) over the C
+ABI of ``libgdn.so`` (declared in ``include/gdn.h``). Each function here has the name of its C entry point and
 only marshals arguments: torch CUDA tensors supply device memory and the
 current CUDA stream; every step of the computation runs in the library's
 sm_100a kernels. There is no CPU or PyTorch fallback: if ``libgdn.so`` is
@@ -14,11 +14,10 @@ Agnes-3.0-Flash Preview model card, 架构 table (gated RMS-norm).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
-from typing import NamedTuple, Optional
+from typing import NamedTuple
 
 import torch
 
@@ -546,105 +545,37 @@ def gdn_attention_status(workspace, stream=None) -> int:
 
 # ------------------------------------------------------------------ paged cache
 # These calls take a few microseconds on the GPU when a step is small, so their
-# checks touch each tensor once or twice and build no message unless one fails.
-_DTYPE3 = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float16: GDN_F16}
-_HALF = (torch.bfloat16, torch.float16)
-_HERE_NOW = contextlib.nullcontext()
-_fn = {}
+# tensors are checked and marshalled by a compiled extension (csrc/
+# paged_binding.cpp); the functions here hold names, defaults and documentation.
+_ext = None
 
 
-def _entry(name):
-    """A C entry point, looked up once."""
-    fn = _fn.get(name)
-    if fn is None:
-        fn = _fn[name] = getattr(load(), name)
-    return fn
+def _binding():
+    """The extension, bound to the loaded libgdn.so. Raises if it has not been built."""
+    global _ext
+    if _ext is None:
+        lib = load()
+        path = os.path.join(_HERE, "_paged.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build it with "
+                "`python -m gated_delta_rule_106_b200._build` (nvcc, g++)")
+        from . import _paged as ext
+        ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "gdn_page_plan", "gdn_qk_norm_rope", "gdn_paged_attention_decode",
+            "gdn_paged_attention_decode_workspace")])
+        _ext = ext
+    return _ext
 
 
-def _dtype3(t: torch.dtype, name) -> int:
-    code = _DTYPE3.get(t)
-    if code is None:
-        raise TypeError(f"{name}: unsupported dtype {t}; use torch.bfloat16, float16 or float32")
-    return code
-
-
-def _one_device(*tensors) -> int:
-    """The index of the CUDA device that all given tensors are on."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()               # -1 on the CPU
-            if d != dev:
-                if d < 0:
-                    raise ValueError("libgdn takes CUDA tensors only (no CPU path)")
-                if dev is not None:
-                    raise ValueError(f"tensors on cuda:{dev} and cuda:{d}: one device is needed")
-                dev = d
-    return dev
-
-
-def _on(dev, stream):
-    """Makes device `dev` and `stream` current for the allocations and the launch
-    of a call, so that buffers made for it belong to the stream that uses them."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        if stream.device_index != dev:
-            raise ValueError(f"stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
-        return torch.cuda.stream(stream)
-    if dev != torch._C._cuda_getDevice():
-        return torch.cuda.device(dev)
-    return _HERE_NOW
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _dense(t, shape, name, dtype):
-    """A contiguous tensor of this shape and dtype (None: not given)."""
-    if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
-        _expect(t, shape, name, dtype)
-
-
-def _rows32(t, N, name):
-    """Row stride of an int32 [N, M] tensor with dense rows."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != N:
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected ({N}, max_pages)")
-    if t.dtype is not torch.int32:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
-    if stride[1] != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: rows must be contiguous")
-    return stride[0] if N > 1 else shape[1]               # one row: no stride is used
-
-
-def _cache_strides(t, name, shape, dtype):
-    """(page, token, head) strides of a [pages, page_size, H_kv, D] cache view."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    page, token, head, one = t.stride()
-    if one != 1:
-        raise ValueError(f"{name}: each row of {shape[3]} values must be contiguous")
-    if 1 in shape:                       # the stride of a dimension of one is never used
-        page, token, head = (n if size > 1 else shape[3]
-                             for n, size in zip((page, token, head), shape))
-    return page, token, head
-
-
-def _head_stride(t, shape, name, dtype):
-    """Row stride of [n, H, D] with dense heads."""
-    if t.shape != shape or t.dtype is not dtype:
-        _expect(t, shape, name, dtype, contiguous=False)
-    row, head, one = t.stride()
-    if one != 1 or (head != shape[2] and shape[1] != 1):
-        raise ValueError(f"{name}: trailing dimensions must be contiguous")
-    return row if shape[0] > 1 else shape[1] * shape[2]
+def _on(stream, tensor):
+    """Makes `stream` current for the allocations and the launch of a call, so that
+    buffers made for it belong to the stream that uses them."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=tensor.device)
+    if stream.device != tensor.device:
+        raise ValueError(f"stream of {stream.device}, tensors on {tensor.device}")
+    return torch.cuda.stream(stream)
 
 
 class PagePlan(NamedTuple):
@@ -670,37 +601,19 @@ def gdn_page_plan(lens, want, block_table, free_pages, free_count, page_size, *,
     (token_capacity entries; -1 and 0 behind the last). Growth that does not fit
     is refused from the first such request on. lens, want and free_count stay as
     they are: adopt new_lens and new_count to go on. Returns a PagePlan."""
-    N, P = lens.numel(), free_pages.numel()
-    if slot_map is not None:
-        if token_capacity is not None and token_capacity != slot_map.numel():
-            raise ValueError("token_capacity is not slot_map's length")
-        token_capacity = slot_map.numel()
-    if token_capacity is None:
-        raise ValueError("give token_capacity or slot_map")
-    i32 = torch.int32
-    _dense(lens, (N,), "lens", i32)
-    _dense(want, (N,), "want", i32)
-    row = _rows32(block_table, N, "block_table")
-    _dense(free_pages, (P,), "free_pages", i32)
-    _dense(free_count, (1,), "free_count", i32)
-    _dense(new_lens, (N,), "new_lens", i32)
-    _dense(cu_new, (N + 1,), "cu_new", i32)
-    _dense(slot_map, (token_capacity,), "slot_map", i32)
-    _dense(positions, (token_capacity,), "positions", i32)
-    _dense(new_count, (1,), "new_count", i32)
-    _dense(info, (4,), "info", i32)
-    dev = _one_device(lens, want, block_table, free_pages, free_count, new_lens, cu_new, slot_map,
-                      positions, new_count, info)
-    with _on(dev, stream):
-        def buf(t, n):
-            return torch.empty(n, dtype=i32, device=lens.device) if t is None else t
-        out = PagePlan(buf(new_lens, N), buf(cu_new, N + 1), buf(slot_map, token_capacity),
-                       buf(positions, token_capacity), buf(new_count, 1), buf(info, 4))
-        _check("gdn_page_plan", _entry("gdn_page_plan")(
-            lens.data_ptr(), want.data_ptr(), N, block_table.data_ptr(), row,
-            block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(), P, page_size,
-            token_capacity, *[t.data_ptr() for t in out], _raw_stream(dev)))
-    return out
+    if stream is not None:
+        with _on(stream, lens):
+            return gdn_page_plan(
+                lens, want, block_table, free_pages, free_count, page_size,
+                token_capacity=token_capacity, new_lens=new_lens, cu_new=cu_new,
+                slot_map=slot_map, positions=positions, new_count=new_count, info=info)
+    r = (_ext or _binding()).page_plan(
+        lens, want, block_table, free_pages, free_count, page_size,
+        -1 if token_capacity is None else token_capacity, new_lens, cu_new, slot_map, positions,
+        new_count, info)
+    if r.__class__ is int:
+        raise GdnError("gdn_page_plan", r)
+    return PagePlan._make(r)
 
 
 def gdn_rope_inv_freq(rope_dims, base=1e7, *, factor=1.0, context=0, beta_fast=32.0,
@@ -711,12 +624,12 @@ def gdn_rope_inv_freq(rope_dims, base=1e7, *, factor=1.0, context=0, beta_fast=3
     if out is None:
         out = torch.empty(rope_dims // 2, dtype=torch.float64,
                           device="cuda" if device is None else device)
-    _dense(out, (rope_dims // 2,), "out", torch.float64)
-    dev = _one_device(out)
-    with _on(dev, stream):
-        _check("gdn_rope_inv_freq", _entry("gdn_rope_inv_freq")(
-            rope_dims, base, factor, context, beta_fast, beta_slow, out.data_ptr(),
-            _raw_stream(dev)))
+    _expect(out, (rope_dims // 2,), "out", torch.float64)
+    address = _ptr(out)
+    with torch.cuda.device(out.device):
+        _check("gdn_rope_inv_freq", load().gdn_rope_inv_freq(
+            rope_dims, base, factor, context, beta_fast, beta_slow, address,
+            _stream(stream, out.device)))
     return out
 
 
@@ -729,75 +642,24 @@ def gdn_qk_norm_rope(q, k, v, k_cache=None, v_cache=None, *, slot_map=None, q_no
     [num_pages, page_size, H_kv, D] (strided views; bf16 or fp16) at slot_map [T]
     (a slot outside the cache marks padding; None: token t at slot t). q, or k
     and v, may be None. Returns q_out [T, H_q, D] in the caches' dtype."""
-    x = q if q is not None else k
-    if x is None or (k is None) != (v is None) or (k is None) != (k_cache is None) or \
-            (k is None) != (v_cache is None):
-        raise ValueError("give q, or k and v with both caches, or all")
-    if x.dim() != 3:
-        raise ValueError(f"q, k, v: {x.dim()} dimensions, expected [T, H, D]")
-    T, H_q, D = x.shape
-    dtype = x.dtype
-    H_kv = P = page = qs = ks = vs = 0
-    k_str = v_str = (0, 0, 0)
-    if q is None:
-        H_q = 0
-        if q_out is not None:
-            raise ValueError("q_out without q")
-    else:
-        qs = _head_stride(q, (T, H_q, D), "q", dtype)
-    if k is not None:
-        H_kv = k.shape[1]
-        shape = (T, H_kv, D)
-        ks = _head_stride(k, shape, "k", dtype)
-        vs = _head_stride(v, shape, "v", dtype)
-        P, page = k_cache.shape[:2]
-        shape = (P, page, H_kv, D)
-        k_str = _cache_strides(k_cache, "k_cache", shape, k_cache.dtype)
-        v_str = _cache_strides(v_cache, "v_cache", shape, k_cache.dtype)
-        if out_dtype is not None and out_dtype is not k_cache.dtype:
-            raise ValueError(f"out_dtype {out_dtype}: q_out has the caches' dtype")
-        out_dtype = k_cache.dtype
-    elif out_dtype is None:
-        out_dtype = q_out.dtype if q_out is not None else torch.float16
-    if out_dtype not in _HALF:
-        raise ValueError(f"caches and q_out are bf16 or fp16, got {out_dtype}")
-    _dense(q_out, (T, H_q, D), "q_out", out_dtype)
-    w = q_norm_w if q_norm_w is not None else k_norm_w
-    if w is not None:
-        _dense(q_norm_w, (D,), "q_norm_w", w.dtype)
-        _dense(k_norm_w, (D,), "k_norm_w", w.dtype)
-    _dense(slot_map, (T,), "slot_map", torch.int32)
-    R, axes = 0, 1
-    if inv_freq is not None:
-        if positions is None:
-            raise ValueError("rotary needs positions")
-        R = 2 * inv_freq.numel()
-        _dense(inv_freq, (R // 2,), "inv_freq", torch.float64)
-        if positions.dim() == 1:
-            _dense(positions, (T,), "positions", torch.int32)
-        else:
-            axes = 3
-            _dense(positions, (3, T), "positions", torch.int32)
-    elif positions is not None:
-        raise ValueError("positions without inv_freq")
-    dev = _one_device(x, k, v, k_cache, v_cache, slot_map, q_norm_w, k_norm_w, positions,
-                      inv_freq, q_out)
-    xd = _dtype3(dtype, "q, k, v")
-    wd = GDN_F32 if w is None else _dtype3(w.dtype, "norm weights")
-    with _on(dev, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty((T, H_q, D), dtype=out_dtype, device=q.device)
-        _check("gdn_qk_norm_rope", _entry("gdn_qk_norm_rope")(
-            _addr(q), qs, _addr(k), ks, _addr(v), vs, xd, _addr(q_norm_w), _addr(k_norm_w), wd,
-            eps, _addr(positions), axes, _addr(inv_freq), R, 1 if interleaved else 0, rope_scale,
-            _addr(slot_map), T, H_q, H_kv, D, _addr(q_out), _addr(k_cache), *k_str,
-            _addr(v_cache), *v_str, P, page, _DTYPE3[out_dtype], _raw_stream(dev)))
-    return q_out
+    if stream is not None:
+        with _on(stream, q if q is not None else k):
+            return gdn_qk_norm_rope(
+                q, k, v, k_cache, v_cache, slot_map=slot_map, q_norm_w=q_norm_w,
+                k_norm_w=k_norm_w, positions=positions, inv_freq=inv_freq,
+                interleaved=interleaved, rope_scale=rope_scale, eps=eps, q_out=q_out,
+                out_dtype=out_dtype)
+    r = (_ext or _binding()).qk_norm_rope(
+        q, k, v, k_cache, v_cache, slot_map, q_norm_w, k_norm_w, positions, inv_freq, interleaved,
+        rope_scale, eps, q_out, out_dtype)
+    if r.__class__ is int:
+        raise GdnError("gdn_qk_norm_rope", r)
+    return r
 
 
 def gdn_paged_attention_decode_workspace(H_q, H_kv, head_dim=ATTN_HEAD_DIM) -> int:
     """Bytes of workspace gdn_paged_attention_decode needs (any N, any lengths)."""
-    return _entry("gdn_paged_attention_decode_workspace")(H_q, H_kv, head_dim)
+    return int(load().gdn_paged_attention_decode_workspace(H_q, H_kv, head_dim))
 
 
 def gdn_paged_attention_decode(q, k_cache, v_cache, block_table, kv_lens, *, gate=None,
@@ -809,43 +671,13 @@ def gdn_paged_attention_decode(q, k_cache, v_cache, block_table, kv_lens, *, gat
     max_pages] (int32). gate [N, H_q, D] bf16: times sigmoid(gate). lse [N, H_q]
     fp32 receives the log of the softmax sums. Returns o [N, H_q, D] (o_dtype,
     bf16 unless given). A sequence of length 0 gives zeros."""
-    if q.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError(f"q: {q.dim()} dimensions, expected [N, H_q, D]; k_cache: "
-                         f"{k_cache.dim()}, expected [num_pages, page_size, H_kv, D]")
-    q_shape, shape, dtype = q.shape, k_cache.shape, k_cache.dtype
-    N, H_q, D = q_shape
-    P, page, H_kv, Dk = shape
-    if dtype not in _HALF:
-        raise ValueError(f"caches are bf16 or fp16, got {dtype}")
-    if Dk != D:
-        raise ValueError(f"k_cache: head dim {Dk}, q has {D}")
-    k_str = _cache_strides(k_cache, "k_cache", shape, dtype)
-    v_str = _cache_strides(v_cache, "v_cache", shape, dtype)
-    qs = _head_stride(q, q_shape, "q", dtype)
-    row = _rows32(block_table, N, "block_table")
-    _dense(kv_lens, (N,), "kv_lens", torch.int32)
-    gs = _head_stride(gate, q_shape, "gate", torch.bfloat16) if gate is not None else 0
-    if o is not None:
-        if o_dtype is not None and o_dtype is not o.dtype:
-            raise ValueError(f"o: dtype {o.dtype}, expected {o_dtype}")
-        o_dtype = o.dtype
-        _dense(o, q_shape, "o", o_dtype)
-    elif o_dtype is None:
-        o_dtype = torch.bfloat16
-    od = _dtype3(o_dtype, "o")
-    _dense(lse, (N, H_q), "lse", torch.float32)
-    dev = _one_device(q, k_cache, v_cache, block_table, kv_lens, gate, o, lse, workspace)
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty(q_shape, dtype=o_dtype, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(
-                max(gdn_paged_attention_decode_workspace(H_q, H_kv, D), 256),
-                dtype=torch.uint8, device=q.device)
-        _check("gdn_paged_attention_decode", _entry("gdn_paged_attention_decode")(
-            q.data_ptr(), qs, k_cache.data_ptr(), *k_str, v_cache.data_ptr(), *v_str,
-            _DTYPE3[dtype], P, page, block_table.data_ptr(), row, block_table.shape[1],
-            kv_lens.data_ptr(), _addr(gate), gs, N, H_q, H_kv, D,
-            D ** -0.5 if scale is None else scale, o.data_ptr(), od, _addr(lse),
-            workspace.data_ptr(), workspace.nbytes, _raw_stream(dev)))
-    return o
+    if stream is not None:
+        with _on(stream, q):
+            return gdn_paged_attention_decode(
+                q, k_cache, v_cache, block_table, kv_lens, gate=gate, scale=scale, o=o,
+                o_dtype=o_dtype, lse=lse, workspace=workspace)
+    r = (_ext or _binding()).paged_attention_decode(
+        q, k_cache, v_cache, block_table, kv_lens, gate, scale, o, o_dtype, lse, workspace)
+    if r.__class__ is int:
+        raise GdnError("gdn_paged_attention_decode", r)
+    return r

@@ -1,7 +1,8 @@
-"""Build libgdn.so (all CUDA sources in csrc/) for sm_100a with nvcc.
+"""Build libgdn.so (all CUDA sources in csrc/) for sm_100a with nvcc, and the
+Python extension ``_paged.so`` (csrc/paged_binding.cpp) with the host compiler.
 
-Objects go to ``_build/`` at the repository root; the shared library is written
-next to this file so that it is loaded in-tree. ``python -m
+Objects go to ``_build/`` at the repository root; the shared libraries are written
+next to this file so that they are loaded in-tree. ``python -m
 gated_delta_rule_106_b200._build`` rebuilds what is stale.
 """
 from __future__ import annotations
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BINDING = os.path.join(PKG, "_paged.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -61,11 +64,34 @@ def _compile(src, extra, verbose):
     return obj
 
 
+def _build_binding(verbose):
+    src = os.path.join(CSRC, "paged_binding.cpp")
+    if not _stale(BINDING, [src, os.path.join(INCLUDE, "gdn.h"), __file__]):
+        return
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", os.path.join(base, "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           src, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        sys.stderr.write(r.stdout + r.stderr)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libgdn.so; return its path."""
+    """Compile every csrc/*.cu for sm_100a and link libgdn.so, build the Python
+    extension; return the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     if force:
-        for f in glob.glob(os.path.join(OBJDIR, "*.o")):
+        for f in glob.glob(os.path.join(OBJDIR, "*.o")) + glob.glob(BINDING):
             os.remove(f)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     srcs = _sources()
@@ -78,6 +104,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_binding(verbose)
     return LIB
 
 

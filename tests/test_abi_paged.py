@@ -189,15 +189,6 @@ def test_binding_checks(lib):
         a(o_dtype=torch.float64)
     with pytest.raises(ValueError, match="out: shape"):
         gdn.gdn_rope_inv_freq(64, out=f)
-    class Fake:
-        def __init__(self, n):
-            self.n = n
-
-        def get_device(self):
-            return self.n
-    with pytest.raises(ValueError, match="one device is needed"):
-        gdn._one_device(Fake(0), None, Fake(1))
-    assert gdn._one_device(None, Fake(3), Fake(3)) == 3
 
 
 def test_plain_plan_form():
