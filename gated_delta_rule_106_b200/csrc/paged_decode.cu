@@ -43,6 +43,7 @@ constexpr int kCWarps = 4;                  // computing warps
 constexpr int kPhases = 3;                  // see Ranges
 constexpr int kMaxBase = 2 * 160;           // CTAs at once
 constexpr int kMaxRanges = kPhases * kMaxBase;
+constexpr int kAhead = 8;                   // blocks that table entries are called in ahead
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 template <int D, int NT>
@@ -128,11 +129,19 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 16 bytes to shared memory; zeros instead (and no read) with real = false
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real = true) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes to shared memory under an L2 policy; zeros instead (and no read)
+// with real = false
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real,
+                                           uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(real ? 16 : 0), "l"(policy)
                : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 // arrives on the barrier once this thread's copies so far have landed
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -226,18 +235,29 @@ __device__ __forceinline__ int blocks_of(const PagedDecodeArgs& a, int len) {
   return len_ok(a, len) ? (int)(((int64_t)len + TOK - 1) / TOK) : 0;
 }
 
-// V = 2 or 4 output values of one (sequence, head): gate and round
+// The gate of V = 2 or 4 values of one (sequence, head).
+template <int V> struct Gate { __nv_bfloat162 v[V / 2]; };
 template <int V>
-__device__ __forceinline__ void put_out(const PagedDecodeArgs& a, int64_t row, int n, int h,
-                                        int d, float (&y)[V]) {
+__device__ __forceinline__ Gate<V> load_gate(const PagedDecodeArgs& a, int n, int h, int d) {
+  Gate<V> g;
   if (a.gate) {
-    const __nv_bfloat162* g = reinterpret_cast<const __nv_bfloat162*>(
+    const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(
         static_cast<const __nv_bfloat16*>(a.gate) + n * a.gate_row_stride + (int64_t)h * a.D + d);
 #pragma unroll
+    for (int i = 0; i < V / 2; ++i) g.v[i] = src[i];
+  }
+  return g;
+}
+// V output values of one (sequence, head) row: gate and round
+template <int V>
+__device__ __forceinline__ void put_out(const PagedDecodeArgs& a, int64_t row, int d,
+                                        const Gate<V>& gate, float (&y)[V]) {
+  if (a.gate) {
+#pragma unroll
     for (int i = 0; i < V / 2; ++i) {
-      const float2 v = __bfloat1622float2(g[i]);
-      y[2 * i] /= 1.0f + __expf(-v.x);
-      y[2 * i + 1] /= 1.0f + __expf(-v.y);
+      const float2 v = __bfloat1622float2(gate.v[i]);
+      y[2 * i] = __fdividef(y[2 * i], 1.0f + __expf(-v.x));        // within 2 ulp
+      y[2 * i + 1] = __fdividef(y[2 * i + 1], 1.0f + __expf(-v.y));
     }
   }
   const int64_t at = row * a.D + d;
@@ -282,8 +302,6 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
   __shared__ int trouble;
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the join may take its place on the chip while this runs
-  asm volatile("griddepcontrol.launch_dependents;");
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -340,6 +358,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     const uint32_t dst0 = smem_u32(sm) + (is_v ? C::kV : 0) +
                           (row0 + lane / LPR) * C::kRow + (lane % LPR) * 16;
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
+    // cached rows are read once: they leave L2 before the table, queries and gates
+    uint64_t once;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     // the unit whose rows are looked up, one ahead of the unit being copied, so
     // that the table's latency passes behind the copies: range, units to its end,
     // sequence, key-value head, block; the sequence's length and blocks
@@ -353,7 +374,14 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       nb = (int)(((int64_t)len + kTok - 1) / kTok);
     };
     int page[E], in_page[E];
+    // With the rows of three blocks per SM in flight a read from HBM takes ~5 us;
+    // what is needed later is called into L2 before: table entries some blocks
+    // ahead, and the gates when their sequence starts.
     auto lookup = [&] {
+      if (lead && lane < 2) {
+        const int64_t j = ((int64_t)blk + kAhead + 4 * lane) * kTok / a.page_size;
+        if (j < a.max_pages) prefetch_l2(a.table + (int64_t)n * a.table_row_stride + j);
+      }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const uint32_t t = (uint32_t)blk * kTok + row0 + lane + 32 * e;
@@ -509,13 +537,19 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int i = 0; i < RB; ++i)
           cp_async16(dst + (r0 + i * RPI) * C::kRow,
-                     cache + max(o[i], (int64_t)0) + (lane % LPR) * 8, o[i] >= 0);
+                     cache + max(o[i], (int64_t)0) + (lane % LPR) * 8, o[i] >= 0, once);
       }
       if (lead && first_now) {
         const Th* q = static_cast<const Th*>(a.q) + b.n * a.q_row_stride + (int64_t)b.g * p.G * D;
         for (int i = lane; i < p.G * LPR; i += 32)
           cp_async16(smem_u32(sm) + st * C::kStage + C::kQ + (i / LPR) * C::kRow +
                      (i % LPR) * 16, q + i * 8);
+        if (a.gate) {
+          const char* g = reinterpret_cast<const char*>(
+              static_cast<const __nv_bfloat16*>(a.gate) + b.n * a.gate_row_stride +
+              (int64_t)b.g * p.G * D);
+          for (int i = lane * 128; i < p.G * D * 2; i += 32 * 128) prefetch_l2(g + i);
+        }
       }
       if (lane == 0) {
         if (lead) {
@@ -719,6 +753,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         for (int w = 0; w < C::kPWarps; ++w) bad |= wrong_page[st][w];
         for (int i = tid; i < p.G * (D / 4); i += 32 * kCWarps) {
           const int h = i / (D / 4), d = 4 * (i % (D / 4));
+          const int hq = b.g * p.G + h;
+          const Gate<4> gate = load_gate<4>(a, b.n, hq, d);
           float M = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kCWarps; ++w) M = fmaxf(M, piece_ml[w][h].x);
@@ -736,12 +772,11 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             y[3] += f * v.w;
           }
           if (bad) L = __int_as_float(0x7fc00000);
-          const int hq = b.g * p.G + h;
           if (b.piece < 0) {
             const float inv = 1.f / L;
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] *= inv;
-            put_out<4>(a, (int64_t)b.n * a.Hq + hq, b.n, hq, d, y);
+            put_out<4>(a, (int64_t)b.n * a.Hq + hq, d, gate, y);
             if (a.lse && d == 0) a.lse[(int64_t)b.n * a.Hq + hq] = (M + log2f(L)) * kLn2;
           } else {
             const int64_t at = ((int64_t)b.range * 2 + b.piece) * p.G + h;
@@ -755,6 +790,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     }
     if (dead) atomicMax(&trouble, 3);           // a wait ran out: more than bad input
   }
+  // the join takes its place on the chip as CTAs end (allowed from the start on, its
+  // blocks sit beside the running ones: 0.5 to 3 us more at most sizes)
+  asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   if (tid == 0) p.flag[blockIdx.x] = trouble == 3 ? 1 : trouble;
 }
@@ -782,7 +820,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     for (int i = tid; i < a.Hkv * (D / 4); i += kJoinThreads) {
       const int hq = i / (D / 4) * p.G + h, d = 4 * (i % (D / 4));
       float y[4] = {v, v, v, v};
-      put_out<4>(a, (int64_t)n * a.Hq + hq, n, hq, d, y);
+      put_out<4>(a, (int64_t)n * a.Hq + hq, d, load_gate<4>(a, n, hq, d), y);
       if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = ok ? -INFINITY : v;
     }
   }
@@ -856,7 +894,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     }
     return make_float2(M, L);
   };
-  auto finish = [&](const int4& j, float2 ml, float (&y)[K][V]) {
+  struct Gates { Gate<V> g[K]; };
+  auto gates = [&](const int4& j) {
+    Gates r;
+#pragma unroll
+    for (int k = 0; k < K; ++k) r.g[k] = load_gate<V>(a, j.x, j.y * p.G + h, (k * 32 + lane) * V);
+    return r;
+  };
+  auto finish = [&](const int4& j, float2 ml, const Gates& g, float (&y)[K][V]) {
     const int hq = j.y * p.G + h;
     const int64_t row = (int64_t)j.x * a.Hq + hq;
     const float inv = 1.f / ml.y;
@@ -864,7 +909,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     for (int k = 0; k < K; ++k) {
 #pragma unroll
       for (int e = 0; e < V; ++e) y[k][e] *= inv;
-      put_out<V>(a, row, j.x, hq, (k * 32 + lane) * V, y[k]);
+      put_out<V>(a, row, (k * 32 + lane) * V, g.g[k], y[k]);
     }
     if (a.lse && lane == 0) a.lse[row] = (ml.x + log2f(ml.y)) * kLn2;
   };
@@ -875,13 +920,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   const bool many = mine.w && mine.z - c + 1 > kFewPieces;
   float y[K][V];
   if (mine.w && !many) {
+    const Gates g = gates(mine);
     const float2 ml = gather(c, mine, 0, 1, y);
-    finish(mine, ml, y);
+    finish(mine, ml, g, y);
   }
   if (!__syncthreads_or(many)) return;
   for (int w = 0; w < kJoinWarps && c0 + w < ranges; ++w) {
     const int4 j = entry[w];
     if (!j.w || j.z - (c0 + w) + 1 <= kFewPieces) continue;
+    const Gates g = gates(j);
     const float2 ml = gather(c0 + w, j, warp, kJoinWarps, y);
     __syncthreads();                           // the last turn's sums are read
 #pragma unroll
@@ -895,7 +942,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
 #pragma unroll
         for (int e = 0; e < V; ++e)
           for (int i = 1; i < kJoinWarps; ++i) y[k][e] += acc[i][(k * 32 + lane) * V + e];
-      finish(j, ml, y);
+      finish(j, ml, g, y);
     }
   }
 }
