@@ -373,7 +373,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       len = (int)min((int64_t)max(len, 0), cap);
       nb = (int)(((int64_t)len + kTok - 1) / kTok);
     };
-    int page[E], in_page[E];
+    int page[E] = {}, in_page[E];                       // in_page < 0: no such row
     // With the rows of three blocks per SM in flight a read from HBM takes ~5 us;
     // what is needed later is called into L2 before: table entries some blocks
     // ahead, and the gates when their sequence starts.
@@ -385,12 +385,11 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const uint32_t t = (uint32_t)blk * kTok + row0 + lane + 32 * e;
-        page[e] = -2;                              // no such row
+        in_page[e] = -1;
         if (t < (uint32_t)len) {
           const uint32_t j = t / (uint32_t)a.page_size;
           in_page[e] = (int)(t - j * a.page_size);
-          page[e] = a.table[(int64_t)n * a.table_row_stride + j];
-          if (page[e] < 0 || page[e] >= a.num_pages) page[e] = -1;
+          page[e] = a.table[(int64_t)n * a.table_row_stride + j];   // looked at a unit later
         }
       }
     };
@@ -480,8 +479,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       bool wrong = false;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        off[e] = page[e] < 0 ? -1 : page[e] * cs.page + in_page[e] * cs.token + g * cs.head;
-        wrong |= page[e] == -1;
+        const bool in = in_page[e] >= 0, ok = in && page[e] >= 0 && page[e] < a.num_pages;
+        off[e] = ok ? page[e] * cs.page + in_page[e] * cs.token + g * cs.head : -1;
+        wrong |= in && !ok;
       }
       bad |= __any_sync(0xffffffffu, wrong);       // a warp's own rows
       const bool bad_now = bad, first_now = first;
