@@ -28,6 +28,8 @@
 // own shared memory at its end. Sequences cut between CTAs leave un-normalised
 // pieces (max, sum, O) in the workspace; a second small kernel joins them in
 // CTA order.
+#include <cudaTypedefs.h>
+
 #include <atomic>
 
 #include "gdn_common.cuh"
@@ -51,10 +53,14 @@ struct Cfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;     // 16-token tiles per warp and block
   static constexpr int kTok = 16 * kTiles * kCWarps;  // tokens per block
   static constexpr int kHeads = 8 * NT;               // head columns
-  static constexpr int kRow = 2 * D + 16;             // bytes per shared-memory row
-  static constexpr int kV = kTok * kRow;              // offsets within a stage
-  static constexpr int kQ = 2 * kTok * kRow;
-  static constexpr int kStage = kQ + kHeads * kRow;
+  // A stage holds the K, then the V rows of a block, each as D / 64 column chunks
+  // [kTok rows][128 bytes] whose 16-byte units are permuted within a row as TMA's
+  // 128-byte swizzle does: unit j of row r is at j ^ (r % 8).
+  static constexpr int kChunk = kTok * 128;
+  static constexpr int kV = kTok * 2 * D;
+  static constexpr int kStage = 2 * kV;
+  static constexpr int kQRow = 2 * D + 16;            // queries behind the stages, padded rows
+  static constexpr int kQStage = kHeads * kQRow;
   // copying warps, half for K, half for V: at D = 128 a row is half a warp's copy
   // and its lookup counts more
   static constexpr int kPWarps = D == 128 && NT == 1 ? 8 : 4;
@@ -62,12 +68,13 @@ struct Cfg {
   static constexpr int kRuns = D == 64 ? 64 : 256;      // runs of sequences that are summed
   static constexpr int kCtasPerSm = D == 64 && NT == 1 ? 2 : 1;
   static constexpr int kStages = D == 64 && NT == 2 ? 5 : 3;
-  static constexpr int kSmem = kStages * kStage;
+  static constexpr int kSmem = 1024 + kStages * (kStage + kQStage);   // 1024 to align
   static constexpr int kBatch = D == 256 && NT == 2 ? 2 : 4;   // fragments loaded ahead
-  static constexpr int kPad = D + 4;                  // floats per head when pieces meet
+  // floats per head when pieces meet (padded against bank conflicts where there is room)
+  static constexpr int kPad = D == 256 && NT == 2 ? D : D + 4;
   // two CTAs per SM: 228 KB with 1 KB of the system's and ~1.5 KB of barriers and sums each
   static_assert(kCtasPerSm == 1 || kSmem + 2560 <= 114 * 1024, "two CTAs fit");
-  static_assert(kCWarps * kHeads * kPad * 4 <= kQ, "pieces meet in a block's K and V rows");
+  static_assert(kCWarps * kHeads * kPad * 4 <= kStage, "pieces meet in a block's K and V rows");
 };
 
 enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
@@ -117,6 +124,8 @@ struct PagedParams {
   int G;
   float sl2;               // scale * log2(e)
   int* status;             // workspace word 0
+  int box;                 // rows per TMA copy, or 0: rows are copied by cp.async
+  bool k_token_first, v_token_first;    // the order of the maps' middle dimensions
   int base;                // CTAs that run at once; more in the grid are taken over
   int* flag;               // [grid] what each CTA met: 0, 1 (a wait ran out), 2 (bad input)
   int4* join;              // [grid] {n, g, last range, 1} for the piece that starts in a range
@@ -139,6 +148,20 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
                "l"(src), "r"(real ? 16 : 0), "l"(policy)
                : "memory");
+}
+// Box at column x, (y, z) = (head, token) or (token, head) and page of a cache.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                        int page, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(page),
+      "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+// The same answer in all lanes, so that a warp leaves its loop together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kLimitNs));
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -286,10 +309,13 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D, int NT, class Th>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
-paged_split_kernel(const __grid_constant__ PagedParams p) {
+paged_split_kernel(const __grid_constant__ PagedParams p,
+                   const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<D, NT>;
   constexpr int kTok = C::kTok;
-  extern __shared__ __align__(128) uint8_t sm[];
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[C::kStages], empty[C::kStages], meet;
   __shared__ BlockDesc desc[C::kStages];
   __shared__ int wrong_page[C::kStages][C::kPWarps];    // met by each copying warp
@@ -305,15 +331,18 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], 33 * C::kPWarps);
+      // TMA: the leading lanes of two copying warps and the queries' copies;
+      // else every lane's copies and the leading lanes
+      mbar_init(&full[i], p.box ? 2 + 32 : 33 * C::kPWarps);
       mbar_init(&empty[i], kCWarps);
     }
     mbar_init(&meet, 32 * kCWarps);
     mbar_init(&asked_full, 1);
-    mbar_init(&asked_free, C::kPWarps);
+    mbar_init(&asked_free, p.box ? 2 : C::kPWarps);
     fence_mbar_init();
     trouble = 0;
   }
+  if (tid < C::kStages * C::kPWarps) (&wrong_page[0][0])[tid] = 0;
   const int per = (a.N + C::kRuns - 1) / C::kRuns;  // a run per thread, the first kRuns threads
   const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
   const int len0 = n0 < n1 ? a.kv_lens[n0] : 0;
@@ -347,16 +376,21 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 
   if (warp >= kCWarps) {
     // ------------------------------------------------------------- copies --
-    // Even warps copy K rows, odd ones V rows, each an even share of the block;
-    // the first also the queries. A row of D values takes D / 8 lanes.
+    // Even warps copy K rows, odd ones V rows, the first also the queries. With TMA
+    // two warps are enough: a lane takes a box of rows of one page. Else each has
+    // an even share of the block's rows, and a row of D values takes D / 8 lanes.
+    const bool tma = p.box != 0;
     constexpr int LPR = D / 8, RPI = 32 / LPR;
     constexpr int kRows = 2 * kTok / C::kPWarps, E = kRows / 32;
     const bool is_v = (warp - kCWarps) & 1, lead = warp == kCWarps;
     const int row0 = (warp - kCWarps) / 2 * kRows;
     const Th* cache = static_cast<const Th*>(is_v ? a.v_cache : a.k_cache);
     const PageStrides cs = is_v ? a.vs : a.ks;
-    const uint32_t dst0 = smem_u32(sm) + (is_v ? C::kV : 0) +
-                          (row0 + lane / LPR) * C::kRow + (lane % LPR) * 16;
+    const uint32_t side = smem_u32(sm) + (is_v ? C::kV : 0);
+    const uint32_t dst0 = side + (row0 + lane / LPR) * 128 + (lane % LPR) / 8 * C::kChunk +
+                          (((lane % 8) ^ (lane / LPR)) << 4);
+    const CUtensorMap* map = is_v ? &v_map : &k_map;
+    const bool token_first = is_v ? p.v_token_first : p.k_token_first;
     const int64_t cap = (int64_t)a.max_pages * a.page_size;
     // cached rows are read once: they leave L2 before the table, queries and gates
     uint64_t once;
@@ -364,6 +398,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     // the unit whose rows are looked up, one ahead of the unit being copied, so
     // that the table's latency passes behind the copies: range, units to its end,
     // sequence, key-value head, block; the sequence's length and blocks
+    const bool idle = tma && warp - kCWarps >= 2;
     int range = blockIdx.x, n = 0, g = 0, blk = 0, len = 0, nb = 0;
     int64_t u = 0, r1 = 0;
     bool first = true, begins = true, bad = false;
@@ -384,9 +419,10 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const uint32_t t = (uint32_t)blk * kTok + row0 + lane + 32 * e;
+        const uint32_t row = tma ? lane * p.box : row0 + lane + 32 * e;
+        const uint32_t t = (uint32_t)blk * kTok + row;
         in_page[e] = -1;
-        if (t < (uint32_t)len) {
+        if (t < (uint32_t)len && (!tma || (e == 0 && row < (uint32_t)kTok))) {
           const uint32_t j = t / (uint32_t)a.page_size;
           in_page[e] = (int)(t - j * a.page_size);
           page[e] = a.table[(int64_t)n * a.table_row_stride + j];   // looked at a unit later
@@ -449,7 +485,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     };
     auto ask = [&] {
       if (lead && lane == 0) {
-        if (answers > 0 && !mbar_wait_bounded(&asked_free, (answers - 1) & 1, kLimitNs)) late = true;
+        if (answers > 0 && !mbar_wait_bounded(&asked_free, (answers - 1) & 1, kLimitNs))
+          late = true;
         else ask_cta(&answer, &asked_full);
       }
       asked = true;
@@ -458,7 +495,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     auto refill = [&] {
       while (u >= r1 && steal) {
         if (!asked) ask();
-        if (!mbar_wait_bounded(&asked_full, answers & 1, kLimitNs)) { late = true; break; }
+        if (!warp_wait(&asked_full, answers & 1)) { late = true; break; }
         range = given_cta(&answer);
         asked = false;
         ++answers;
@@ -469,9 +506,11 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         else enter();
       }
     };
-    enter();
-    refill();
-    if (u < r1) lookup();
+    if (!idle) {
+      enter();
+      refill();
+      if (u < r1) lookup();
+    }
     int it = 0;
     for (; u < r1; ++it) {
       const int st = it % C::kStages;
@@ -484,6 +523,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         wrong |= in && !ok;
       }
       bad |= __any_sync(0xffffffffu, wrong);       // a warp's own rows
+      const int page_now = page[0], token_now = in_page[0];
+      const bool box_now = off[0] >= 0;
       const bool bad_now = bad, first_now = first;
       const bool last_blk = blk + 1 == nb, last = last_blk || u + 1 == r1;
       BlockDesc b;
@@ -521,29 +562,31 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
       if (steal && !asked && r1 - u <= 3) ask();
       refill();
       if (u < r1) lookup();
-      if (!mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs)) break;
-      const uint32_t dst = dst0 + st * C::kStage;
-      // no branch per row, and the shuffles of eight rows ahead of their copies:
-      // a lane's turn at a row then costs its instructions, not their latencies
-      constexpr int RB = 8;
+      if (!warp_wait(&empty[st], ((it / C::kStages) & 1) ^ 1)) break;
+      if (!tma) {
+        // no branch per row, and the shuffles of eight rows ahead of their copies:
+        // a lane's turn at a row then costs its instructions, not their latencies
+        const uint32_t dst = dst0 + st * C::kStage;
+        constexpr int RB = 8;
 #pragma unroll
-      for (int r0 = 0; r0 < kRows; r0 += RB * RPI) {
-        int64_t o[RB];
+        for (int r0 = 0; r0 < kRows; r0 += RB * RPI) {
+          int64_t o[RB];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          const int r = r0 + i * RPI;
-          o[i] = __shfl_sync(0xffffffffu, off[r / 32], r % 32 + lane / LPR);
+          for (int i = 0; i < RB; ++i) {
+            const int r = r0 + i * RPI;
+            o[i] = __shfl_sync(0xffffffffu, off[r / 32], r % 32 + lane / LPR);
+          }
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+            cp_async16((dst ^ (((i * RPI) & 7) << 4)) + (r0 + i * RPI) * 128,
+                       cache + max(o[i], (int64_t)0) + (lane % LPR) * 8, o[i] >= 0, once);
         }
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-          cp_async16(dst + (r0 + i * RPI) * C::kRow,
-                     cache + max(o[i], (int64_t)0) + (lane % LPR) * 8, o[i] >= 0, once);
       }
       if (lead && first_now) {
         const Th* q = static_cast<const Th*>(a.q) + b.n * a.q_row_stride + (int64_t)b.g * p.G * D;
         for (int i = lane; i < p.G * LPR; i += 32)
-          cp_async16(smem_u32(sm) + st * C::kStage + C::kQ + (i / LPR) * C::kRow +
-                     (i % LPR) * 16, q + i * 8);
+          cp_async16(smem_u32(sm) + C::kStages * C::kStage + st * C::kQStage +
+                     (i / LPR) * C::kQRow + (i % LPR) * 16, q + i * 8);
         if (a.gate) {
           const char* g = reinterpret_cast<const char*>(
               static_cast<const __nv_bfloat16*>(a.gate) + b.n * a.gate_row_stride +
@@ -559,32 +602,52 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         }
         wrong_page[st][warp - kCWarps] = bad_now;
         if (bad_now) atomicMax(&trouble, 2);
-        mbar_arrive(&full[st]);
+        if (!tma) mbar_arrive(&full[st]);
       }
-      cp_async_arrive(&full[st]);
+      if (!tma || lead) cp_async_arrive(&full[st]);
+      if (tma) {
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box_now));
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * p.box * 2 * D);
+        __syncwarp();
+        if (box_now) {
+          const uint32_t dst = side + st * C::kStage + lane * p.box * 128;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            tma_box(dst + x * C::kChunk, map, x * 64, token_first ? token_now : b.g,
+                    token_first ? b.g : token_now, page_now, &full[st], once);
+        }
+      }
     }
-    // end mark, then wait for the copies in flight
-    const int st = it % C::kStages;
-    const bool fine = mbar_wait_bounded(&empty[st], ((it / C::kStages) & 1) ^ 1, kLimitNs);
-    if (fine) {
-      if (tid == 32 * kCWarps) desc[st].flags = kEnd;
-      if (lane == 0) mbar_arrive(&full[st]);
-      mbar_arrive(&full[st]);
+    // end mark, then wait for the copies in flight (those that a computing warp
+    // still waits for need no wait here)
+    if (!idle) {
+      const int st = it % C::kStages;
+      const bool fine = warp_wait(&empty[st], ((it / C::kStages) & 1) ^ 1);
+      if (fine) {
+        if (lead && lane == 0) desc[st].flags = kEnd;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        if (!tma || lead) mbar_arrive(&full[st]);
+      } else {
+        late = true;
+        for (int i = max(0, it - C::kStages); tma && i < it; ++i)
+          mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kLimitNs);
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     // an answer that nobody waited for (only after a wait ran out)
-    if (asked && lead && lane == 0 && !late)
-      late = !mbar_wait_bounded(&asked_full, answers & 1, kLimitNs);
-    if ((!fine || late) && lane == 0) atomicMax(&trouble, 3);
+    if (asked && lead && lane == 0 && !mbar_wait_bounded(&asked_full, answers & 1, kLimitNs))
+      late = true;
+    if (late) atomicMax(&trouble, 3);
   } else {
     // ------------------------------------------------------------ compute --
     const int row = lane >> 2, qd = lane & 3;
     const int mj = lane >> 3, mi = lane & 7;
     // ldmatrix row addresses: matrix mj, row mi
     const int tok0 = warp * 16 * C::kTiles;
-    const uint32_t k_off = (uint32_t)((tok0 + (mj & 1) * 8 + mi) * C::kRow + (mj >> 1) * 16);
-    const uint32_t v_off = (uint32_t)((tok0 + (mj >> 1) * 8 + mi) * C::kRow + (mj & 1) * 16);
-    const uint32_t q_off = (uint32_t)(mi * C::kRow + mj * 16);    // two k-steps per load
+    const uint32_t k_off = (tok0 + (mj & 1) * 8 + mi) * 128 + (((mj >> 1) ^ mi) << 4);
+    const uint32_t v_off = C::kV + (tok0 + (mj >> 1) * 8 + mi) * 128 + (((mj & 1) ^ mi) << 4);
+    const uint32_t q_off = mi * C::kQRow + mj * 16;               // two k-steps per load
     const uint32_t smb = smem_u32(sm);
     uint32_t qf[NT][D / 16][2];
     float o[NT][D / 16][4];
@@ -593,7 +656,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
     bool dead = false;
     for (int it = 0; !dead; ++it) {
       const int st = it % C::kStages;
-      if (!mbar_wait_bounded(&full[st], (it / C::kStages) & 1, kLimitNs)) { dead = true; break; }
+      if (!warp_wait(&full[st], (it / C::kStages) & 1)) { dead = true; break; }
       const BlockDesc b = desc[st];
       if (b.flags & kEnd) break;
       const uint32_t base = smb + st * C::kStage;
@@ -603,7 +666,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) {
             uint32_t r[4];
-            ldsm4(base + C::kQ + t * 8 * C::kRow + q_off + kk * 64, r);
+            ldsm4(smb + C::kStages * C::kStage + st * C::kQStage + t * 8 * C::kQRow + q_off + kk * 64,
+                  r);
             qf[t][2 * kk][0] = r[0];
             qf[t][2 * kk][1] = r[1];
             qf[t][2 * kk + 1][0] = r[2];
@@ -616,7 +680,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           l[t][0] = l[t][1] = 0.f;
         }
       }
-      const int nt = b.ntok - tok0;            // this warp's tokens (rows behind them are zeros)
+      const int nt = b.ntok - tok0;            // this warp's tokens
       if (nt > 0) {
         // the fragments of all K tiles, then of all V tiles, in batches: one is
         // loaded ahead of the products that use it
@@ -624,11 +688,13 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         uint32_t fr[2][B][4];
         auto load = [&](int i) {                   // batch i of 2 NB
           const int tt = i / KB % TT, kb = i % KB;
-          const uint32_t at = base + tt * 16 * C::kRow + kb * B * 32;
+          const uint32_t at = base + tt * 16 * 128;
 #pragma unroll
-          for (int e = 0; e < B; ++e) {
-            if (i < NB) ldsm4(at + k_off + e * 32, fr[i & 1][e]);
-            else ldsm4_t(at + C::kV + v_off + e * 32, fr[i & 1][e]);
+          for (int e = 0; e < B; ++e) {            // 16 dims: two 16-byte units of a row
+            const int kk = kb * B + e;
+            const uint32_t unit = (uint32_t)(kk & 3) << 5, chunk = kk / 4 * C::kChunk;
+            if (i < NB) ldsm4(((at + k_off) ^ unit) + chunk, fr[i & 1][e]);
+            else ldsm4_t(((at + v_off) ^ unit) + chunk, fr[i & 1][e]);
           }
         };
         load(0);
@@ -709,6 +775,20 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         for (int i = 0; i < NB; ++i) {
           const int tt = i / KB, vb = i % KB;
           if (i + 1 < NB) load(NB + i + 1);
+          if (nt < 16 * TT) {
+            // what lies behind the last row must not meet a weight of 0: it may be the
+            // rest of a page, or of an earlier block, and hold anything
+            const int t0 = 16 * tt + 2 * qd;
+            const uint32_t keep0 = (t0 < nt ? 0xffffu : 0u) | (t0 + 1 < nt ? 0xffff0000u : 0u);
+            const uint32_t keep1 = (t0 + 8 < nt ? 0xffffu : 0u) | (t0 + 9 < nt ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int e = 0; e < B; ++e) {
+              fr[(NB + i) & 1][e][0] &= keep0;
+              fr[(NB + i) & 1][e][1] &= keep0;
+              fr[(NB + i) & 1][e][2] &= keep1;
+              fr[(NB + i) & 1][e][3] &= keep1;
+            }
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -725,7 +805,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
         uint8_t* stage = sm + st * C::kStage;
         float* mine = reinterpret_cast<float*>(stage) + warp * C::kHeads * C::kPad;
         mbar_arrive(&meet);
-        if (!mbar_wait_bounded(&meet, meets & 1, kLimitNs)) { dead = true; break; }
+        if (!warp_wait(&meet, meets & 1)) { dead = true; break; }
         ++meets;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -745,7 +825,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
           }
         }
         mbar_arrive(&meet);
-        if (!mbar_wait_bounded(&meet, meets & 1, kLimitNs)) { dead = true; break; }
+        if (!warp_wait(&meet, meets & 1)) { dead = true; break; }
         ++meets;
         const float* all = reinterpret_cast<const float*>(stage);
         int bad = 0;
@@ -784,6 +864,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p) {
             if (d == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, L);
           }
         }
+        fence_proxy_async_smem();              // written here before the next copies land
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
@@ -951,6 +1032,50 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
 constexpr int max_ranges(int D) { return D == 64 ? kMaxRanges : kMaxRanges / 2; }
 constexpr size_t kHeadBytes = 256 + kMaxRanges * 4 + kMaxRanges * 16;
 
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = found.load(std::memory_order_relaxed);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* ptr = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    found.store(fn, std::memory_order_relaxed);
+  }
+  return fn;
+}
+// A cache as [page][token][head][D] or [page][head][token][D], the smaller stride
+// inside; boxes of p.box tokens of one head by 64 dims. False where a map cannot
+// say it: each stride has to be a multiple of the one inside it, below 2^40 bytes.
+bool make_map(CUtensorMap* map, const void* base, const PageStrides& s, const PagedParams& p,
+              bool* token_first) {
+  auto fn = map_encoder();
+  if (!fn) return false;
+  const int page_size = p.a.page_size, heads = p.a.Hkv;
+  *token_first = heads == 1 || (page_size > 1 && s.token < s.head);
+  const cuuint64_t size[2] = {(cuuint64_t)(*token_first ? page_size : heads),
+                              (cuuint64_t)(*token_first ? heads : page_size)};
+  cuuint64_t strides[3] = {(cuuint64_t)(*token_first ? s.token : s.head) * 2,
+                           (cuuint64_t)(*token_first ? s.head : s.token) * 2,
+                           (cuuint64_t)s.page * 2};
+  if (size[0] == 1) strides[0] = (cuuint64_t)p.a.D * 2;        // never used
+  if (size[1] == 1) strides[1] = strides[0] * size[0];
+  if (p.a.num_pages == 1) strides[2] = strides[1] * size[1];
+  if (strides[1] % strides[0] || strides[2] % strides[1] || strides[2] >> 40) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.a.D, size[0], size[1], (cuuint64_t)p.a.num_pages};
+  const cuuint32_t rows = (cuuint32_t)p.box;
+  const cuuint32_t box[4] = {64, *token_first ? rows : 1, *token_first ? 1 : rows, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn(map,
+            p.a.kv_dtype == GDN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            4, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int NT, class Th>
 cudaError_t launch_split(PagedParams p, int sms) {
   using C = Cfg<D, NT>;
@@ -970,7 +1095,14 @@ cudaError_t launch_split(PagedParams p, int sms) {
   const int64_t cap = (int64_t)p.a.max_pages * p.a.page_size;
   const int64_t most = (cap + C::kTok - 1) / C::kTok * p.a.N * p.a.Hkv;
   const int grid = most >= kStealUnits * (int64_t)p.base ? kPhases * p.base : p.base;
-  paged_split_kernel<D, NT, Th><<<grid, C::kThreads, C::kSmem, p.a.stream>>>(p);
+  // copies by TMA where the page size has a factor of 8 rows
+  CUtensorMap k_map{}, v_map{};
+  p.box = p.a.page_size & -p.a.page_size;
+  if (p.box > C::kTok) p.box = C::kTok;
+  if (p.box < 8 || !make_map(&k_map, p.a.k_cache, p.a.ks, p, &p.k_token_first) ||
+      !make_map(&v_map, p.a.v_cache, p.a.vs, p, &p.v_token_first))
+    p.box = 0;
+  paged_split_kernel<D, NT, Th><<<grid, C::kThreads, C::kSmem, p.a.stream>>>(p, k_map, v_map);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join starts while the split's last CTAs end, and waits for them
@@ -1010,7 +1142,7 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  PagedParams p;
+  PagedParams p{};
   p.a = a;
   p.G = a.Hq / a.Hkv;
   p.sl2 = a.scale * 1.4426950408889634f;
