@@ -3,20 +3,29 @@
 // row j of sequence n at page table[n][j / page_size], offset j % page_size.
 //
 // The K and V rows cross HBM once, so bytes bound it (2 * G FLOP per cached
-// byte for a group of G query heads, a few percent of the tensor rate). The work
-// is cut evenly: the units are (sequence, key-value head, block of 64 or 128 tokens) in
-// that order, the grid is as many CTAs as fit on the chip at once, and CTA c
-// takes units [c U / C, (c + 1) U / C) whatever sequences they belong to. So
-// one long sequence spreads over all SMs, and ragged lengths leave none idle;
-// the host needs no lengths (every CTA sums kv_lens itself).
+// byte for a group of G query heads, a few percent of the tensor rate): 256
+// sequences of 4097 tokens (24 / 4 heads, D = 256, 4.3 GB) take 616 us, 7.0 TB/s,
+// and 675 us where the power cap holds the clocks at 1.6 GHz; one sequence of
+// 131071 tokens 88 us, 6.1 TB/s.
 //
-// In a CTA two warps copy, one the K and one the V rows: they look up each
-// row's page and have it copied to shared memory (16-byte cp.async to rows padded
-// by 16 bytes, so ldmatrix meets no bank conflict), kStages blocks ahead and
-// across sequence ends. Row-sized bulk copies (cp.async.bulk of 2 D bytes) need
-// fewer instructions but the lanes of a warp issue them one after the other,
-// ~70 cycles each: 2.07 ms against XXX ms for 256 sequences of 4097
-// tokens. Four warps compute, 16 tokens of the block each, on mma.sync m16n8k16:
+// The work is cut evenly: the units are (sequence, key-value head, block of 64 or
+// 128 tokens) in that order, and CTAs take ranges of units whatever sequences
+// they belong to (see Ranges). So one long sequence spreads over all SMs, ragged
+// lengths leave none idle, and the host needs no lengths: every CTA sums kv_lens
+// itself. The cuts depend on the lengths and the chip alone, never on which CTA
+// comes first, so equal calls give equal bits.
+//
+// In a CTA copying warps fill a ring of three blocks in shared memory, ahead of the
+// computing warps and across sequence ends. They look each page up and copy its
+// rows by TMA, boxes of rows x 64 dims with the 128-byte swizzle (ldmatrix then
+// meets no bank conflict); where pages have no factor of 8 rows, by 16-byte
+// cp.async to the same places. What was measured on the way (256 x 4097 tokens):
+// row-sized cp.async.bulk 2.07 ms (a warp's lanes issue them one after the other,
+// ~70 cycles each), cp.async by two warps 0.80, by four 0.64 (0.80 under the power
+// cap: the copies' instructions cost energy), TMA 0.62 (0.68).
+//
+// Four warps compute, 16-token tiles, on mma.sync m16n8k16 (the legacy warp MMA: a
+// tcgen05 tile of 128 rows would be mostly empty, and the tensor pipe is 8 % busy):
 //   S^T = K Q^T   (16 tokens x 8 heads), then
 //   O^T += V^T P^T (D x 8 heads), P^T turned in registers by movmatrix.
 // Tokens or head dims fill the 16 rows and the group's heads the 8 columns, so
@@ -24,13 +33,15 @@
 // and sum in fp32 and rescales only when a score passes the max by 8 (2^8).
 // P goes in as high and low 16-bit parts: what rounding it once would cost
 // (2^-9 relative for bf16) is as much as the output's own rounding, and the
-// tensor pipe has room. The warps' pieces of a sequence meet in the block's
-// own shared memory at its end. Sequences cut between CTAs leave un-normalised
-// pieces (max, sum, O) in the workspace; a second small kernel joins them in
-// CTA order.
+// tensor pipe has room (2 % of the time). For fp32 outputs bf16 takes a third part
+// (1.3e-6 of the output without it, 1e-7 with it). The warps' pieces of a sequence
+// meet in the block's own shared memory at its end. Sequences cut between ranges
+// leave un-normalised pieces (max, sum, O) in the workspace; a second small kernel
+// joins them in order (3 to 4 us).
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "gdn_common.cuh"
 #include "launch.h"
@@ -125,6 +136,7 @@ struct PagedParams {
   float sl2;               // scale * log2(e)
   int* status;             // workspace word 0
   int box;                 // rows per TMA copy, or 0: rows are copied by cp.async
+  int copy_warps;          // copying warps at work
   bool k_token_first, v_token_first;    // the order of the maps' middle dimensions
   int base;                // CTAs that run at once; more in the grid are taken over
   int* flag;               // [grid] what each CTA met: 0, 1 (a wait ran out), 2 (bad input)
@@ -232,21 +244,20 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two floats as 16-bit high parts, and what they leave as 16-bit low parts
-__device__ __forceinline__ void split2(float a, float b, __half, uint32_t& hi, uint32_t& lo) {
+// two floats rounded to 16 bits; a and b keep what that leaves
+__device__ __forceinline__ uint32_t take2(float& a, float& b, __half) {
   const __half2 h = __floats2half2_rn(a, b);
   const float2 f = __half22float2(h);
-  const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&r);
+  a -= f.x;
+  b -= f.y;
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void split2(float a, float b, __nv_bfloat16, uint32_t& hi,
-                                       uint32_t& lo) {
+__device__ __forceinline__ uint32_t take2(float& a, float& b, __nv_bfloat16) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   const float2 f = __bfloat1622float2(h);
-  const __nv_bfloat162 r = __floats2bfloat162_rn(a - f.x, b - f.y);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&r);
+  a -= f.x;
+  b -= f.y;
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ bool len_ok(const PagedDecodeArgs& a, int len) {
@@ -331,14 +342,14 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      // TMA: the leading lanes of two copying warps and the queries' copies;
-      // else every lane's copies and the leading lanes
-      mbar_init(&full[i], p.box ? 2 + 32 : 33 * C::kPWarps);
+      // the leading lanes of the copying warps, and each lane's own copies (TMA:
+      // the queries' alone, by the first warp)
+      mbar_init(&full[i], p.copy_warps + 32 * (p.box ? 1 : C::kPWarps));
       mbar_init(&empty[i], kCWarps);
     }
     mbar_init(&meet, 32 * kCWarps);
     mbar_init(&asked_full, 1);
-    mbar_init(&asked_free, p.box ? 2 : C::kPWarps);
+    mbar_init(&asked_free, p.copy_warps);
     fence_mbar_init();
     trouble = 0;
   }
@@ -377,8 +388,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
   if (warp >= kCWarps) {
     // ------------------------------------------------------------- copies --
     // Even warps copy K rows, odd ones V rows, the first also the queries. With TMA
-    // two warps are enough: a lane takes a box of rows of one page. Else each has
-    // an even share of the block's rows, and a row of D values takes D / 8 lanes.
+    // a lane takes a box of rows of one page, and as many warps work as the boxes
+    // need (lanes issue one after the other). Else each has an even share of the
+    // block's rows, and a row of D values takes D / 8 lanes.
     const bool tma = p.box != 0;
     constexpr int LPR = D / 8, RPI = 32 / LPR;
     constexpr int kRows = 2 * kTok / C::kPWarps, E = kRows / 32;
@@ -398,7 +410,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     // the unit whose rows are looked up, one ahead of the unit being copied, so
     // that the table's latency passes behind the copies: range, units to its end,
     // sequence, key-value head, block; the sequence's length and blocks
-    const bool idle = tma && warp - kCWarps >= 2;
+    const bool idle = warp - kCWarps >= p.copy_warps;
+    const int box_row = ((warp - kCWarps) / 2 + lane * (p.copy_warps / 2)) * p.box;
     int range = blockIdx.x, n = 0, g = 0, blk = 0, len = 0, nb = 0;
     int64_t u = 0, r1 = 0;
     bool first = true, begins = true, bad = false;
@@ -419,7 +432,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const uint32_t row = tma ? lane * p.box : row0 + lane + 32 * e;
+        const uint32_t row = tma ? box_row : row0 + lane + 32 * e;
         const uint32_t t = (uint32_t)blk * kTok + row;
         in_page[e] = -1;
         if (t < (uint32_t)len && (!tma || (e == 0 && row < (uint32_t)kTok))) {
@@ -610,7 +623,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
         if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * p.box * 2 * D);
         __syncwarp();
         if (box_now) {
-          const uint32_t dst = side + st * C::kStage + lane * p.box * 128;
+          const uint32_t dst = side + st * C::kStage + box_row * 128;
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
             tma_box(dst + x * C::kChunk, map, x * 64, token_first ? token_now : b.g,
@@ -685,6 +698,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
         // the fragments of all K tiles, then of all V tiles, in batches: one is
         // loaded ahead of the products that use it
         constexpr int TT = C::kTiles, B = C::kBatch, KB = D / 16 / B, NB = TT * KB;
+        constexpr int PP = std::is_same<Th, __half>::value ? 2 : 3;
         uint32_t fr[2][B][4];
         auto load = [&](int i) {                   // batch i of 2 NB
           const int tt = i / KB % TT, kb = i % KB;
@@ -722,7 +736,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
             for (int e = 0; e < 4; ++e)
               x[tt][t][e] = 16 * tt + row + 8 * (e >> 1) < nt ? total(s[t], e) * p.sl2 : -INFINITY;
         }
-        uint32_t hi[TT][NT][2], lo[TT][NT][2];
+        uint32_t part[PP][TT][NT][2];              // P's 16-bit parts, high to low
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float top[2];
@@ -758,16 +772,14 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
           const float mb = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll
           for (int tt = 0; tt < TT; ++tt) {
-            const float p0 = ex2(x[tt][t][0] - ma), p1 = ex2(x[tt][t][1] - mb);
-            const float p2 = ex2(x[tt][t][2] - ma), p3 = ex2(x[tt][t][3] - mb);
+            float p0 = ex2(x[tt][t][0] - ma), p1 = ex2(x[tt][t][1] - mb);
+            float p2 = ex2(x[tt][t][2] - ma), p3 = ex2(x[tt][t][3] - mb);
             l[t][0] += p0 + p2;
             l[t][1] += p1 + p3;
-            split2(p0, p1, Th(), hi[tt][t][0], lo[tt][t][0]);
-            split2(p2, p3, Th(), hi[tt][t][1], lo[tt][t][1]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              hi[tt][t][e] = transpose8x8(hi[tt][t][e]);
-              lo[tt][t][e] = transpose8x8(lo[tt][t][e]);
+            for (int i = 0; i < PP; ++i) {
+              part[i][tt][t][0] = transpose8x8(take2(p0, p1, Th()));
+              part[i][tt][t][1] = transpose8x8(take2(p2, p3, Th()));
             }
           }
         }
@@ -792,11 +804,13 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int e = 0; e < B; ++e)
-              mma16816<Th>(o[t][vb * B + e], fr[(NB + i) & 1][e], hi[tt][t][0], hi[tt][t][1]);
+            for (int part_i = 0; part_i < PP; ++part_i) {
+              if (part_i == 2 && p.a.o_dtype != GDN_F32) break;
 #pragma unroll
-            for (int e = 0; e < B; ++e)
-              mma16816<Th>(o[t][vb * B + e], fr[(NB + i) & 1][e], lo[tt][t][0], lo[tt][t][1]);
+              for (int e = 0; e < B; ++e)
+                mma16816<Th>(o[t][vb * B + e], fr[(NB + i) & 1][e], part[part_i][tt][t][0],
+                             part[part_i][tt][t][1]);
+            }
           }
         }
       }
@@ -1095,13 +1109,22 @@ cudaError_t launch_split(PagedParams p, int sms) {
   const int64_t cap = (int64_t)p.a.max_pages * p.a.page_size;
   const int64_t most = (cap + C::kTok - 1) / C::kTok * p.a.N * p.a.Hkv;
   const int grid = most >= kStealUnits * (int64_t)p.base ? kPhases * p.base : p.base;
-  // copies by TMA where the page size has a factor of 8 rows
+  // copies by TMA where the page size has a factor of 8 rows, 16 at D = 256. Against
+  // cp.async: 256 x 4097 tokens, D = 256, pages of 64: 616 us, 666; 64 x 4097, pages of
+  // 16: D = 256 168, 180, D = 128 166, 169, D = 64 182, 193; pages of 8: 191, 180;
+  // 171, 169; 175, 192
   CUtensorMap k_map{}, v_map{};
   p.box = p.a.page_size & -p.a.page_size;
   if (p.box > C::kTok) p.box = C::kTok;
-  if (p.box < 8 || !make_map(&k_map, p.a.k_cache, p.a.ks, p, &p.k_token_first) ||
+  if (p.box < (D == 256 ? 16 : 8) || !make_map(&k_map, p.a.k_cache, p.a.ks, p, &p.k_token_first) ||
       !make_map(&v_map, p.a.v_cache, p.a.vs, p, &p.v_token_first))
     p.box = 0;
+  // a warp for every eight copies of each side
+  p.copy_warps = C::kPWarps;
+  if (p.box) {
+    const int copies = C::kTok / p.box * (D / 64);
+    p.copy_warps = 2 * max(1, min(copies / 8, C::kPWarps / 2));
+  }
   paged_split_kernel<D, NT, Th><<<grid, C::kThreads, C::kSmem, p.a.stream>>>(p, k_map, v_map);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
