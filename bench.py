@@ -1065,6 +1065,27 @@ def profile_case(args):
         # N sequences (--n) of 4096 cached tokens: 64 hold 1.1 GB of cache
         wl = AttentionDecodeWorkload(gdn, dev, 0, 1, n=N)
         run = lambda: (wl.reset(), wl.step(0))
+    elif name == "pdec":
+        # N sequences (--n) of 4097 tokens in shuffled pages of 64
+        L, page = 4097, 64
+        held = -(-L // page)
+        kc, vc = (torch.empty(N * held, page, gdn.ATTN_H_KV, gdn.ATTN_HEAD_DIM,
+                              dtype=torch.float16, device=dev).normal_() for _ in range(2))
+        table = torch.randperm(N * held, device=dev).to(torch.int32).view(N, held)
+        lens = torch.full((N,), L, dtype=torch.int32, device=dev)
+        q = torch.randn(N, gdn.ATTN_H_Q, gdn.ATTN_HEAD_DIM, device=dev).half()
+        gate = torch.randn_like(q, dtype=torch.float32).bfloat16()
+        run = lambda: gdn.gdn_paged_attention_decode(q, kc, vc, table, lens, gate=gate)
+    elif name == "append":
+        # T tokens (--t) of the attention layer, normed, rotated and appended
+        p = {k: v.to(dev) for k, v in gi.attention_inputs(T, seed=0).items()}
+        kc, vc = (torch.empty(-(-T // 64), 64, gdn.ATTN_H_KV, gdn.ATTN_HEAD_DIM,
+                              dtype=torch.float16, device=dev) for _ in range(2))
+        pos = torch.arange(T, dtype=torch.int32, device=dev).repeat(3, 1)
+        inv = gdn.gdn_rope_inv_freq(64, 1e7)
+        run = lambda: gdn.gdn_qk_norm_rope(p["q"], p["k"], p["v"], kc, vc, positions=pos,
+                                           q_norm_w=p["q_norm_w"], k_norm_w=p["k_norm_w"],
+                                           inv_freq=inv)
     else:
         raise SystemExit(f"unknown profile case {name}")
     torch.cuda.synchronize()
@@ -1078,7 +1099,7 @@ def profile_case(args):
 
 
 PROFILE_CASES = ("decode", "dlayer", "prefill", "layer", "varlen", "conv", "norm", "dconv",
-                 "attn", "adec")
+                 "attn", "adec", "pdec", "append")
 
 
 def main():

@@ -621,15 +621,20 @@ def gdn_rope_inv_freq(rope_dims, base=1e7, *, factor=1.0, context=0, beta_fast=3
     """Rotary frequencies base^(-2i / rope_dims) in fp64 [rope_dims / 2] for
     gdn_qk_norm_rope, all divided by `factor`, or with `context` (the trained
     length) by parts: pairs that turn often over it keep their frequency."""
-    if out is None:
-        out = torch.empty(rope_dims // 2, dtype=torch.float64,
-                          device="cuda" if device is None else device)
-    _expect(out, (rope_dims // 2,), "out", torch.float64)
-    address = _ptr(out)
-    with torch.cuda.device(out.device):
-        _check("gdn_rope_inv_freq", load().gdn_rope_inv_freq(
-            rope_dims, base, factor, context, beta_fast, beta_slow, address,
-            _stream(stream, out.device)))
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):              # None: the current one
+        if out is None:
+            out = torch.empty(rope_dims // 2, dtype=torch.float64,
+                              device="cuda" if device is None else device)
+        _expect(out, (rope_dims // 2,), "out", torch.float64)
+        address = _ptr(out)
+        if stream is not None and stream.device != out.device:
+            raise ValueError(f"stream of {stream.device}, tensors on {out.device}")
+        with torch.cuda.device(out.device):
+            _check("gdn_rope_inv_freq", load().gdn_rope_inv_freq(
+                rope_dims, base, factor, context, beta_fast, beta_slow, address,
+                _stream(stream, out.device)))
     return out
 
 

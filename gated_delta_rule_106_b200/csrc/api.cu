@@ -631,6 +631,10 @@ gdn_status gdn_paged_attention_decode(const void* q, int64_t q_row_stride, const
       (gate && gate_row_stride % 8 != 0) || !aligned16(o) || !aligned16(workspace) ||
       !aligned_to(block_table, 4) || !aligned_to(kv_lens, 4) || !aligned_to(lse, 4))
     return GDN_ERR_MISALIGNED;
+  const size_t o_bytes = (size_t)N * row * gdn::elem_bytes(o_dtype);
+  if (overlap(q, ((size_t)(N - 1) * q_row_stride + row) * 2, o, o_bytes) ||
+      (gate && overlap(gate, ((size_t)(N - 1) * gate_row_stride + row) * 2, o, o_bytes)))
+    return GDN_ERR_INVALID_ARG;
   gdn::PagedDecodeArgs a{q, q_row_stride, k_cache, v_cache, ks, vs, kv_dtype, num_pages,
                          page_size, block_table, table_row_stride, max_pages, kv_lens, gate,
                          gate_row_stride, N, H_q, H_kv, head_dim, scale, o, o_dtype, lse,

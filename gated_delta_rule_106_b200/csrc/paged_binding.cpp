@@ -181,7 +181,8 @@ PyObject* guarded(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, F body) 
   }
   return nullptr;
 }
-// the C entry point without the interpreter's lock: a launch can wait for room in the queue
+// the C entry point without the interpreter's lock: a launch can wait for room in the
+// queue. The call must not throw.
 template <class F>
 gdn_status unlocked(F call) {
   gdn_status st;
@@ -342,13 +343,14 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     const int hq = narrow(Hq, "H_q"), hkv = narrow(Hkv, "H_kv"), d = narrow(D, "head_dim"),
               r = narrow(R, "rope_dims"), p = narrow(P, "num_pages"), ps = narrow(page, "page_size");
+    const gdn_dtype out_code = code(out_type, "q_out");
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     const gdn_status st = unlocked([&] {
       return norm_rope_fn(addr(q), qs, addr(k), ks, addr(v), vs, xd, addr(wq), addr(wk), wd, eps,
                           ints(pos), axes, static_cast<const double*>(addr(inv)), r, interleaved,
                           scale, ints(slots), T, hq, hkv, d, addr(q_out), addr(kc), kstr.page,
                           kstr.token, kstr.head, addr(vc), vstr.page, vstr.token, vstr.head, p, ps,
-                          code(out_type, "q_out"), stream);
+                          out_code, stream);
     });
     if (st != GDN_OK) return status(st);
     if (!q) Py_RETURN_NONE;
@@ -391,7 +393,7 @@ PyObject* paged_attention_decode(PyObject*, PyObject* const* args, Py_ssize_t n)
       o_type = o->scalar_type();
       dense(o, q.sizes(), "o", o_type);
     }
-    const gdn_dtype od = code(o_type, "o");
+    const gdn_dtype od = code(o_type, "o"), kv_code = code(type, "caches");
     dense(lse, {N, Hq}, "lse", at::kFloat);
     const float scale = a[6] == Py_None ? 1.0f / sqrtf((float)D) : (float)real(a[6]);
     if (ws && !ws->is_contiguous()) refuse("workspace must be contiguous");
@@ -414,7 +416,7 @@ PyObject* paged_attention_decode(PyObject*, PyObject* const* args, Py_ssize_t n)
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     const gdn_status st = unlocked([&] {
       return decode_fn(q.data_ptr(), qs, kc.data_ptr(), ks.page, ks.token, ks.head, vc.data_ptr(),
-                       vs.page, vs.token, vs.head, code(type, "caches"), p, ps, ints(&table), row,
+                       vs.page, vs.token, vs.head, kv_code, p, ps, ints(&table), row,
                        (int)table.size(1), ints(&lens), addr(gate), gs, n32, hq, hkv, d, scale,
                        o->data_ptr(), od, static_cast<float*>(addr(lse)), ws->data_ptr(),
                        (size_t)ws->nbytes(), stream);

@@ -92,7 +92,7 @@ def test_norm_rope_validation(lib):
 def decode(lib, **kw):
     a = dict(q=A, qs=24 * 256, kc=A, kp=65536, kt=1024, kh=256, vc=A, vp=65536, vt=1024, vh=256,
              kd=F16, P=64, page=64, table=A, row=16, width=16, lens=A, gate=None, gs=0, N=4, Hq=24,
-             Hkv=4, D=256, scale=0.0625, o=A, od=BF16, lse=None, ws=A, wb=1 << 40, s=None)
+             Hkv=4, D=256, scale=0.0625, o=A + STEP, od=BF16, lse=None, ws=A, wb=1 << 40, s=None)
     a.update(kw)
     return lib.gdn_paged_attention_decode(*a.values())
 
@@ -107,10 +107,15 @@ def test_decode_validation(lib):
                dict(table=None), dict(lens=None), dict(o=None), dict(ws=None),
                dict(wb=lib.gdn_paged_attention_decode_workspace(24, 4, 256) - 1)):
         assert decode(lib, **kw) == INVALID, kw
-    for kw in (dict(q=A + 2), dict(qs=24 * 256 + 4), dict(kc=A + 8), dict(vp=65540), dict(o=A + 8),
+    for kw in (dict(q=A + 2), dict(qs=24 * 256 + 4), dict(kc=A + 8), dict(vp=65540), dict(o=A + STEP + 8),
                dict(ws=A + 4), dict(gate=A + 8, gs=24 * 256), dict(gate=A, gs=24 * 256 + 1),
                dict(table=A + 2), dict(lens=A + 1), dict(lse=A + 2)):
         assert decode(lib, **kw) == MISALIGNED, kw
+    # the output over the queries or the gate; more work than is counted
+    for kw in (dict(o=A), dict(o=A + 4 * 24 * 512 - 16), dict(gate=A + STEP, gs=24 * 256)):
+        assert decode(lib, **kw) == INVALID, kw
+    assert decode(lib, N=65535, Hq=65535, Hkv=65535, qs=65535 * 256, width=1 << 25, row=1 << 25,
+                  kp=65535 * 256 * 64, kt=65535 * 256) == UNSUPPORTED
     assert decode(lib, N=0) == OK
     assert lib.gdn_paged_attention_decode_workspace(24, 5, 256) == 0
     assert lib.gdn_paged_attention_decode_workspace(24, 4, 96) == 0

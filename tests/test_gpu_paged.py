@@ -409,6 +409,13 @@ def test_decode_taken_over_ranges(D, H_q, H_kv, N, lo, hi):
         assert float((d / (1e-4 + o[a:a + 16].float().abs())).max()) < 2.0 ** -7
     for _ in range(4):
         assert torch.equal(run_decode(s, workspace=ws), o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = run_decode(s, workspace=ws)
+    for _ in range(2):
+        again.zero_()
+        graph.replay()
+        assert torch.equal(again, o)
     table[1, 0] = P                              # a bad page there, and a bad length
     s["lens"][2] = width * page + 1
     b = run_decode(s, workspace=ws)
@@ -499,6 +506,31 @@ def test_decode_views_shared_pages_and_workspace():
     t = decode_state([3000, 2], 24, 4, 256, 64, F16, seed=9)
     check_decode(t, run_decode(t, workspace=ws))
     check_decode(s, run_decode(s, workspace=ws))
+
+
+@pytest.mark.parametrize("page", [8, 16, 64, 192])
+@pytest.mark.parametrize("D", [64, 256])
+def test_decode_cache_strides(page, D):
+    """Padded pages, tokens and heads (strides that are no multiples of one another),
+    heads cut out of wider rows, one head, one page, in the order given and turned."""
+    lens = [3 * page + 5, page, 1, 2 * page - 1]
+    for H_kv, pad in ((2, (24, 0, 0)), (2, (0, 8, 0)), (3, (0, 0, 64)), (1, (0, 0, 0)),
+                      (1, (8, 64, 0))):
+        for heads_first in (False, True):
+            s = decode_state(lens, 4 * H_kv, H_kv, D, page, BF16, heads_first, seed=page + H_kv)
+            for name in ("kc", "vc"):
+                c = s[name].transpose(1, 2) if heads_first else s[name]
+                P, a, b, _ = c.shape
+                inner = D + pad[2]
+                rows = b * inner + pad[1]
+                wide = torch.full((P, a * rows + pad[0]), float("nan"), dtype=BF16, device=DEV)
+                view = wide.as_strided((P, a, b, D), (a * rows + pad[0], rows, inner, 1))
+                view.copy_(c)
+                s[name] = view.transpose(1, 2) if heads_first else view
+            check_decode(s, run_decode(s))
+    s = decode_state([page - 1], 4, 2, D, page, F16, spare=0)
+    assert s["kc"].shape[0] == 1
+    check_decode(s, run_decode(s))
 
 
 def test_decode_bad_pages_and_lengths():
