@@ -886,7 +886,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     if (dead) atomicMax(&trouble, 3);           // a wait ran out: more than bad input
   }
   // the join takes its place on the chip as CTAs end (allowed from the start on, its
-  // blocks sit beside the running ones: 0.5 to 3 us more at most sizes)
+  // blocks wait beside the running ones: up to 2.5 us more)
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   if (tid == 0) p.flag[blockIdx.x] = trouble == 3 ? 1 : trouble;
