@@ -29,8 +29,8 @@
 //   S^T = K Q^T   (16 tokens x 8 heads), then
 //   O^T += V^T P^T (D x 8 heads), P^T turned in registers by movmatrix.
 // Tokens or head dims fill the 16 rows and the group's heads the 8 columns, so
-// a group of up to 8 heads wastes no rows. Each warp keeps its own running max
-// and sum in fp32 and rescales only when a score passes the max by 8 (2^8).
+// a group of up to 8 heads wastes no rows. Each warp keeps its own reference (near
+// the running max) and sum in fp32 and rescales rarely (kTop below).
 // P goes in as high and low 16-bit parts: what rounding it once would cost
 // (2^-9 relative for bf16) is as much as the output's own rounding, and the
 // tensor pipe has room (2 % of the time). For fp32 outputs bf16 takes a third part
@@ -57,6 +57,11 @@ constexpr int kPhases = 3;                  // see Ranges
 constexpr int kMaxBase = 2 * 160;           // CTAs at once
 constexpr int kMaxRanges = kPhases * kMaxBase;
 constexpr int kAhead = 8;                   // blocks that table entries are called in ahead
+// Weights are 2^(score - m) with m 11 below the highest score when it was set, and m
+// moves when a score passes it by 15: weights reach 2^15, and fp16's smallest steps
+// (2^-24) are 2^-35 of the largest. A long context whose sum is one key's and the
+// rest's of 10^5 keys with weights of 2^-20 each needs that.
+constexpr float kLift = 11.f, kTop = 15.f;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 template <int D, int NT>
@@ -747,8 +752,8 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
             for (int tt = 1; tt < TT; ++tt) top[e] = fmaxf(top[e], fmaxf(x[tt][t][e], x[tt][t][e + 2]));
           }
           const int h0 = 8 * t + 2 * qd;
-          const bool rise = (h0 < p.G && top[0] > m[t][0] + 8.f) ||
-                            (h0 + 1 < p.G && top[1] > m[t][1] + 8.f);
+          const bool rise = (h0 < p.G && top[0] > m[t][0] + kTop) ||
+                            (h0 + 1 < p.G && top[1] > m[t][1] + kTop);
           if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -756,7 +761,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
               mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 4));
               mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 8));
               mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
-              mb = fmaxf(mb, m[t][e]);
+              mb = fmaxf(mb - kLift, m[t][e]);
               const float f = mb == -INFINITY ? 1.f : ex2(m[t][e] - mb);
               m[t][e] = mb;
               l[t][e] *= f;
@@ -767,7 +772,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
               }
             }
           }
-          // a max of -inf (no finite score yet) must not meet itself
+          // a reference of -inf (no finite score yet) must not meet itself
           const float ma = m[t][0] == -INFINITY ? 0.f : m[t][0];
           const float mb = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll

@@ -483,6 +483,28 @@ def test_decode_peaked_and_flat_scores():
     assert bool(o[0, :, 5].isnan().all()) and int(o.isnan().sum()) == 2
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("above", [10.0, 14.0, 17.0])
+def test_decode_one_key_above_many(dtype, above):
+    """One key takes most of the sum and 60000 equal ones share the rest, each with a
+    weight of e^-above of the first's: their common rounding must not add up. 150
+    such sequences over the same pages, so that none is cut into many pieces."""
+    L, D, page = 60001, 64, 64
+    s = decode_state([L, L], 2, 1, D, page, dtype, gate=False, seed=6)
+    s["q"].fill_(1.0)
+    for at in (0, L - 1):                        # the key comes first, or last
+        for n in range(2):
+            pages = s["table"][n].long()
+            s["kc"][pages] = torch.where(s["kc"][pages].isnan(), s["kc"][pages], 0.0)
+            s["vc"][pages] = torch.where(s["vc"][pages].isinf(), s["vc"][pages],
+                                         1 + 0.1 * s["vc"][pages].clamp(-3, 3))
+            s["kc"][pages[at // page], at % page] = above * D ** 0.5 / D
+            s["vc"][pages[at // page], at % page] = -1.0
+        many = dict(s, **{k: s[k].repeat(75, *[1] * (s[k].dim() - 1)) for k in ("q", "table", "lens")})
+        lse = torch.empty(150, 2, device=DEV)
+        check_decode(many, run_decode(many, o_dtype=F32, lse=lse), lse, only=[0, 75, 149])
+
+
 def test_decode_views_shared_pages_and_workspace():
     """q and gate as views, sequences that share pages, k and v in one buffer, one
     workspace for calls of different shapes, contents of it before a call."""
