@@ -66,6 +66,10 @@ template <> struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     u = __ldg(reinterpret_cast<const uint4*>(p));
   }
+  // not through the read-only path: for kernels that start before their inputs are written
+  __device__ __forceinline__ void load_late(const __nv_bfloat16* p) {
+    u = *reinterpret_cast<const uint4*>(p);
+  }
   __device__ __forceinline__ void to_f32(float (&f)[8]) const {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
@@ -81,6 +85,10 @@ template <> struct Raw8<__half> {
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const __half* p) {
     u = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  // not through the read-only path: for kernels that start before their inputs are written
+  __device__ __forceinline__ void load_late(const __half* p) {
+    u = *reinterpret_cast<const uint4*>(p);
   }
   __device__ __forceinline__ void to_f32(float (&f)[8]) const {
     const __half2* h = reinterpret_cast<const __half2*>(&u);
@@ -98,6 +106,10 @@ template <> struct Raw8<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_late(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void to_f32(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;

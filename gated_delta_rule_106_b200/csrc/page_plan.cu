@@ -19,6 +19,7 @@
 // So a call repeated on the same inputs gives the same outputs.
 #include "gdn_common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 
 namespace gdn {
 namespace {
@@ -96,6 +97,8 @@ __global__ void __launch_bounds__(kMaxThreads) page_plan_kernel(const PlanParams
   const Limits lim{(uint32_t)p.token_capacity + 1u, (uint32_t)p.num_pages + 1u};
   const bool writer = blockIdx.x == 0;
   if (tid == 0) sh.refused = 0;
+  let_next_start();
+  wait_for_previous();
 
   // running sums: a run of requests per thread, then over the threads
   const int per = (p.N + threads - 1) / threads;
@@ -260,8 +263,7 @@ cudaError_t launch_page_plan(const PagePlanArgs& a) {
   const int threads = work <= 128 ? 128 : (work <= 512 ? 512 : kMaxThreads);
   const int64_t want = (a.token_capacity + 4 * threads - 1) / (4 * threads);
   const unsigned grid = (unsigned)(want < 1 ? 1 : (want > 148 ? 148 : want));
-  kernel<<<grid, threads, smem, a.stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(kernel, dim3(grid), (unsigned)threads, smem, a.stream, p);
 }
 
 }  // namespace gdn

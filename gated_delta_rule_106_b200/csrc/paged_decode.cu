@@ -45,6 +45,7 @@
 
 #include "gdn_common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace gdn {
@@ -359,6 +360,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     trouble = 0;
   }
   if (tid < C::kStages * C::kPWarps) (&wrong_page[0][0])[tid] = 0;
+  wait_for_previous();
   const int per = (a.N + C::kRuns - 1) / C::kRuns;  // a run per thread, the first kRuns threads
   const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
   const int len0 = n0 < n1 ? a.kv_lens[n0] : 0;
@@ -892,7 +894,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
   }
   // the join takes its place on the chip as CTAs end (allowed from the start on, its
   // blocks wait beside the running ones: up to 2.5 us more)
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_start();
   __syncthreads();
   if (tid == 0) p.flag[blockIdx.x] = trouble == 3 ? 1 : trouble;
 }
@@ -924,7 +926,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
       if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = ok ? -INFINITY : v;
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
+  let_next_start();
   if (blockIdx.x == 0 && h == 0) {
     int f = 0;
     for (int i = tid; i < ranges; i += kJoinThreads) f |= p.flag[i];
@@ -1130,20 +1133,13 @@ cudaError_t launch_split(PagedParams p, int sms) {
     const int copies = C::kTok / p.box * (D / 64);
     p.copy_warps = 2 * max(1, min(copies / 8, C::kPWarps / 2));
   }
-  paged_split_kernel<D, NT, Th><<<grid, C::kThreads, C::kSmem, p.a.stream>>>(p, k_map, v_map);
-  e = cudaGetLastError();
+  e = launch_early(paged_split_kernel<D, NT, Th>, dim3((unsigned)grid), C::kThreads, C::kSmem,
+                   p.a.stream, p, k_map, v_map);
   if (e != cudaSuccess) return e;
-  // the join starts while the split's last CTAs end, and waits for them
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((grid + kJoinWarps - 1) / kJoinWarps), (unsigned)p.G);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = p.a.stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, grid);
+  // the join's CTAs come in while the split's last ones end, and wait for them
+  return launch_early(paged_join_kernel<D>,
+                      dim3((unsigned)((grid + kJoinWarps - 1) / kJoinWarps), (unsigned)p.G),
+                      kJoinThreads, 0, p.a.stream, p, grid);
 }
 
 template <int D, class Th>

@@ -20,6 +20,7 @@
 // There is no barrier.
 #include "gdn_common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 
 namespace gdn {
 namespace {
@@ -91,7 +92,7 @@ __device__ __forceinline__ void do_heads(const NormRopeArgs& p, const Tx* src, T
   auto load = [&](int h) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (h + u * RPW + sub < h1) raw[u].load(src + (int64_t)(h + u * RPW + sub) * D);
+      if (h + u * RPW + sub < h1) raw[u].load_late(src + (int64_t)(h + u * RPW + sub) * D);
       else raw[u].zero();
     }
   };
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPR;
   const int64_t task = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t t = task / shares;
+  let_next_start();
   if (t >= p.T) return;
   const int Hq = p.q ? p.Hq : 0, Hkv = p.k ? p.Hkv : 0;
   // passes of RPW heads: first those of q, then k, then v
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeAr
     for (int i = lane * 128; i < bytes; i += 32 * 128)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
   };
+  wait_for_previous();
   prefetch(q, q0, q1);
   prefetch(k, k0, k1);
   prefetch(v, v0, v1);
@@ -301,13 +304,10 @@ cudaError_t launch_typed(const NormRopeArgs& a) {
   shares = (passes + share_passes - 1) / share_passes;
   const unsigned grid = (unsigned)((a.T * shares + kWarps - 1) / kWarps);
   const int s = (int)shares;
-  if (a.D == 256)
-    qk_norm_rope_kernel<PARTNER, Tx, To, 256><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
-  else if (a.D == 128)
-    qk_norm_rope_kernel<PARTNER, Tx, To, 128><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
-  else
-    qk_norm_rope_kernel<PARTNER, Tx, To, 64><<<grid, kThreads, 0, a.stream>>>(a, s, share_passes);
-  return cudaGetLastError();
+  auto kernel = a.D == 256 ? qk_norm_rope_kernel<PARTNER, Tx, To, 256>
+              : a.D == 128 ? qk_norm_rope_kernel<PARTNER, Tx, To, 128>
+                           : qk_norm_rope_kernel<PARTNER, Tx, To, 64>;
+  return launch_early(kernel, dim3(grid), kThreads, 0, a.stream, a, s, share_passes);
 }
 
 template <class Tx, class To>

@@ -706,3 +706,65 @@ def test_serving_steps_against_the_oracle():
     mine = [table[n, :-(-x // page)].tolist() for n, x in enumerate(lens.tolist())]
     assert sorted(sum(mine, []) + free[:int(count)].tolist()) == list(range(P))
     assert math.isfinite(float(count))
+
+
+def test_captured_step_equals_eager_steps():
+    """A whole decode step (plan, norm + rotary + append, attention, the copies that adopt
+    the plan) captured once and replayed, with a request that never grows; bit for bit
+    the same as the eager calls."""
+    H_q, H_kv, D, page, P, N = 12, 2, 128, 16, 40, 5
+    inv = gdn.gdn_rope_inv_freq(64, 1e6, factor=4.0, context=256)
+    w = torch.randn(D, device=DEV)
+    steps = [[torch.randn(N, H, D, device=DEV).bfloat16() for H in (H_q, H_kv, H_kv)]
+             for _ in range(40)]
+
+    class Server:
+        def __init__(self):
+            self.kc, self.vc = (torch.zeros(P, H_kv, page, D, dtype=BF16, device=DEV).transpose(1, 2)
+                                for _ in range(2))
+            self.table = torch.full((N, 20), -1, dtype=torch.int32, device=DEV)
+            self.free = torch.arange(P, dtype=torch.int32, device=DEV).flip(0).contiguous()
+            self.lens, self.count = i32([0] * N), i32([P])
+            self.grow = i32([1, 1, 0, 1, 1])
+            self.x = [t.clone() for t in steps[0]]
+            self.ws = torch.empty(gdn.gdn_paged_attention_decode_workspace(H_q, H_kv, D),
+                                  dtype=torch.uint8, device=DEV)
+
+        def step(self):
+            p = gdn.gdn_page_plan(self.lens, self.lens + self.grow, self.table, self.free,
+                                  self.count, page, token_capacity=N)
+            # rows of the requests that got a token, in order, padding behind
+            row = torch.searchsorted(p.cu_new, torch.arange(N, device=DEV, dtype=torch.int32),
+                                     right=True, out_int32=True) - 1
+            q, k, v = (t[row.clamp(max=N - 1)] for t in self.x)
+            q = gdn.gdn_qk_norm_rope(q, k, v, self.kc, self.vc, slot_map=p.slot_map, k_norm_w=w,
+                                     q_norm_w=w, positions=p.positions, inv_freq=inv)
+            back = torch.zeros(N, H_q, D, dtype=BF16, device=DEV)
+            back[row.clamp(max=N - 1).long()] = q      # rows of padding end up in the last
+            self.o = gdn.gdn_paged_attention_decode(back, self.kc, self.vc, self.table,
+                                                    p.new_lens * self.grow, workspace=self.ws)
+            self.lens.copy_(p.new_lens)
+            self.count.copy_(p.new_count)
+            return self.o
+
+    eager, captured = Server(), Server()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        Server().step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = captured.step()
+    for xs in steps:
+        for s in (eager, captured):
+            for a, b in zip(s.x, xs):
+                a.copy_(b)
+        o = eager.step()
+        graph.replay()
+        n = 4                                          # the last row may hold padding's queries
+        assert torch.equal(out[:n], o[:n])
+        for name in ("lens", "count", "table", "free", "kc", "vc"):
+            assert torch.equal(getattr(eager, name), getattr(captured, name)), name
+    assert eager.lens.tolist() == [40, 40, 0, 40, 40] and int(eager.count) == P - 12
+    assert not bool(eager.o[2].any())
