@@ -198,12 +198,18 @@ __global__ void __launch_bounds__(kMaxThreads) page_plan_kernel(const PlanParams
     return p.table[(int64_t)m * p.table_row_stride + goal + (int)(w - back[m])];
   };
   const uint32_t first = blockIdx.x * threads + tid, step = gridDim.x * threads;
-  for (uint32_t i = first; i < take_all; i += step) {
+  // where taken page i goes
+  auto taken_at = [&](uint32_t i) -> int64_t {
     const int m = last_le(take, p.N, i);
-    const int held = pp.page.up(p.lens[m]);
-    p.table[(int64_t)m * p.table_row_stride + held + (int)(i - take[m])] = entry(avail - 1 - i);
-  }
-  for (uint32_t v = count + first; v < avail - take_all; v += step) p.free_pages[v] = entry(v);
+    return (int64_t)m * p.table_row_stride + pp.page.up(p.lens[m]) + (int)(i - take[m]);
+  };
+  // A thread's first taken and first returned page are read before its tokens and
+  // written after them, so that the three reads' latencies pass together.
+  const uint32_t put_end = avail - take_all;     // returned pages stay at count .. put_end - 1
+  const bool take_one = first < take_all, put_one = count + first < put_end;
+  const int64_t take_to = take_one ? taken_at(first) : 0;
+  const int take_page = take_one ? entry(avail - 1 - first) : 0;
+  const int put_page = put_one ? entry(count + first) : 0;
 
   // four tokens per thread and round: one search, then forward
   for (int64_t t0 = 4 * (int64_t)first; t0 < p.token_capacity; t0 += 4 * (int64_t)step) {
@@ -242,6 +248,11 @@ __global__ void __launch_bounds__(kMaxThreads) page_plan_kernel(const PlanParams
       }
     }
   }
+  if (take_one) p.table[take_to] = take_page;
+  if (put_one) p.free_pages[count + first] = put_page;
+  for (uint32_t i = first + step; i < take_all; i += step)
+    p.table[taken_at(i)] = entry(avail - 1 - i);
+  for (uint32_t v = count + first + step; v < put_end; v += step) p.free_pages[v] = entry(v);
 }
 
 }  // namespace
