@@ -3,7 +3,7 @@
 //
 // A serving step makes these calls once per layer, and a small one takes 4 to 10 us on
 // the GPU; through ctypes the checks and the 20 to 34 converted arguments took
-// 15, 18 and 30 us on the host. Here they take a microsecond or two. Module
+// 15, 18 and 30 us on the host, launches included. Here a call takes 5 to 8. Module
 // functions take positional arguments only (the Python functions of the package
 // hold the names, defaults and documentation) and return the result, or the
 // gdn_status as an int where the C entry point refused the call.
