@@ -324,7 +324,8 @@ def gdn_chunked_prefill_status(workspace=None, stream=None) -> int:
 
 def gdn_set_wait_limit_ns(ns: int) -> None:
     """Bound (ns) on each wait of the chunked prefill kernel for another CTA's
-    flag; 0 restores the default (2 s). Process-wide."""
+    flag, and of the paged decode's warps for one another; 0 restores the default
+    (2 s). Process-wide."""
     load().gdn_set_wait_limit_ns(int(ns))
 
 

@@ -63,7 +63,11 @@ constexpr int kAhead = 8;                   // blocks that table entries are cal
 // (2^-24) are 2^-35 of the largest. A long context whose sum is one key's and the
 // rest's of 10^5 keys with weights of 2^-20 each needs that.
 constexpr float kLift = 11.f, kTop = 15.f;
-constexpr uint64_t kLimitNs = 2000000000ull;
+// Waits of warps for one another have the caller's bound (gdn_set_wait_limit_ns); at
+// the end of a CTA that gave up, what is still in flight into its shared memory is
+// waited for this long.
+constexpr uint64_t kDrainNs = 2000000000ull;
+constexpr uint64_t kSuspendNs = 1000000ull;
 
 template <int D, int NT>
 struct Cfg {
@@ -145,6 +149,8 @@ struct PagedParams {
   int copy_warps;          // copying warps at work
   bool k_token_first, v_token_first;    // the order of the maps' middle dimensions
   int base;                // CTAs that run at once; more in the grid are taken over
+  uint64_t limit_ns;       // bound of a wait
+  bool poll;               // a bound below kSuspendNs
   int* flag;               // [grid] what each CTA met: 0, 1 (a wait ran out), 2 (bad input)
   int4* join;              // [grid] {n, g, last range, 1} for the piece that starts in a range
   float* ml;               // [grid][2][G][2]
@@ -177,9 +183,31 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
+// Waits for at most p.limit_ns. A try_wait may suspend its warp for longer than a read of
+// global memory takes (a suspend-time operand did not change that): short bounds are
+// polled for.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const PagedParams& p) {
+  auto look = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (look()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (p.poll ? look() : mbar_try_wait(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > p.limit_ns) return false;
+  }
+}
 // The same answer in all lanes, so that a warp leaves its loop together.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kLimitNs));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const PagedParams& p) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, p));
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -345,6 +373,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
   __shared__ int trouble;
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int copied = 0;                                  // blocks whose copies this warp began
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -423,6 +452,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     int64_t u = 0, r1 = 0;
     bool first = true, begins = true, bad = false;
     bool steal = (int)gridDim.x > p.base, asked = false, late = false;
+    bool answer_due = false;                            // lane 0 of the lead: one is on its way
     int answers = 0;
     auto measure = [&] {
       len = (int)min((int64_t)max(len, 0), cap);
@@ -505,9 +535,12 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     };
     auto ask = [&] {
       if (lead && lane == 0) {
-        if (answers > 0 && !mbar_wait_bounded(&asked_free, (answers - 1) & 1, kLimitNs))
+        if (answers > 0 && !wait_bounded(&asked_free, (answers - 1) & 1, p)) {
           late = true;
-        else ask_cta(&answer, &asked_full);
+        } else {
+          ask_cta(&answer, &asked_full);
+          answer_due = true;
+        }
       }
       asked = true;
     };
@@ -515,9 +548,9 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     auto refill = [&] {
       while (u >= r1 && steal) {
         if (!asked) ask();
-        if (!warp_wait(&asked_full, answers & 1)) { late = true; break; }
+        if (!warp_wait(&asked_full, answers & 1, p)) { late = true; break; }
         range = given_cta(&answer);
-        asked = false;
+        asked = answer_due = false;
         ++answers;
         fence_proxy_async_smem();                  // read here before the next answer lands
         __syncwarp();
@@ -582,7 +615,10 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
       if (steal && !asked && r1 - u <= 3) ask();
       refill();
       if (u < r1) lookup();
-      if (!warp_wait(&empty[st], ((it / C::kStages) & 1) ^ 1)) break;
+      if (!warp_wait(&empty[st], ((it / C::kStages) & 1) ^ 1, p)) {
+        late = true;
+        break;
+      }
       if (!tma) {
         // no branch per row, and the shuffles of eight rows ahead of their copies:
         // a lane's turn at a row then costs its instructions, not their latencies
@@ -638,12 +674,11 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
         }
       }
     }
-    // end mark, then wait for the copies in flight (those that a computing warp
+    // end mark, or wait for the copies in flight (those that a computing warp
     // still waits for need no wait here)
     if (!idle) {
       const int st = it % C::kStages;
-      const bool fine = warp_wait(&empty[st], ((it / C::kStages) & 1) ^ 1);
-      if (fine) {
+      if (warp_wait(&empty[st], ((it / C::kStages) & 1) ^ 1, p)) {
         if (lead && lane == 0) desc[st].flags = kEnd;
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
@@ -651,13 +686,13 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
       } else {
         late = true;
         for (int i = max(0, it - C::kStages); tma && i < it; ++i)
-          mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kLimitNs);
+          mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kDrainNs);
       }
     }
+    copied = it;
     asm volatile("cp.async.wait_all;" ::: "memory");
     // an answer that nobody waited for (only after a wait ran out)
-    if (asked && lead && lane == 0 && !mbar_wait_bounded(&asked_full, answers & 1, kLimitNs))
-      late = true;
+    if (answer_due) mbar_wait_bounded(&asked_full, answers & 1, kDrainNs);
     if (late) atomicMax(&trouble, 3);
   } else {
     // ------------------------------------------------------------ compute --
@@ -676,7 +711,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     bool dead = false;
     for (int it = 0; !dead; ++it) {
       const int st = it % C::kStages;
-      if (!warp_wait(&full[st], (it / C::kStages) & 1)) { dead = true; break; }
+      if (!warp_wait(&full[st], (it / C::kStages) & 1, p)) { dead = true; break; }
       const BlockDesc b = desc[st];
       if (b.flags & kEnd) break;
       const uint32_t base = smb + st * C::kStage;
@@ -826,7 +861,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
         uint8_t* stage = sm + st * C::kStage;
         float* mine = reinterpret_cast<float*>(stage) + warp * C::kHeads * C::kPad;
         mbar_arrive(&meet);
-        if (!warp_wait(&meet, meets & 1)) { dead = true; break; }
+        if (!warp_wait(&meet, meets & 1, p)) { dead = true; break; }
         ++meets;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -846,7 +881,7 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
           }
         }
         mbar_arrive(&meet);
-        if (!warp_wait(&meet, meets & 1)) { dead = true; break; }
+        if (!warp_wait(&meet, meets & 1, p)) { dead = true; break; }
         ++meets;
         const float* all = reinterpret_cast<const float*>(stage);
         int bad = 0;
@@ -896,6 +931,10 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
   // blocks wait beside the running ones: up to 2.5 us more)
   let_next_start();
   __syncthreads();
+  // nor may copies be in flight when the CTA ends that computing warps gave up waiting for
+  if (trouble == 3 && p.box)
+    for (int i = max(0, copied - C::kStages); i < copied; ++i)
+      mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kDrainNs);
   if (tid == 0) p.flag[blockIdx.x] = trouble == 3 ? 1 : trouble;
 }
 
@@ -903,6 +942,11 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
 // and end in a later one; also sums up what the CTAs met. A warp takes one
 // range and head; where a sequence has many pieces (a long one, alone), the
 // block's warps share them.
+// Where a wait ran out, a range may have no entry of this call (the CTA that was to
+// write it gave up, or was taken over by one that did) and its place hold anything:
+// then no entry is followed, and every row with tokens becomes NaN. Every block reads
+// all flags for that, beside its entries (0.05 us; as a piece of code of its own behind
+// a loop over the flags 0.3 us, the code being cold each time).
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kFewPieces = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int ranges) {
@@ -912,27 +956,40 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   const PagedDecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c0 = blockIdx.x * kJoinWarps, h = blockIdx.y;
-  // sequences without a token, or with a length out of range: nothing of the
-  // split kernel's is needed for them
-  for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
-    const int len = a.kv_lens[n];
-    const bool ok = len_ok(a, len);
-    if (ok && len > 0) continue;
-    const float v = ok ? 0.f : __int_as_float(0x7fc00000);
-    for (int i = tid; i < a.Hkv * (D / 4); i += kJoinThreads) {
-      const int hq = i / (D / 4) * p.G + h, d = 4 * (i % (D / 4));
-      float y[4] = {v, v, v, v};
-      put_out<4>(a, (int64_t)n * a.Hq + hq, d, load_gate<4>(a, n, hq, d), y);
-      if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = ok ? -INFINITY : v;
+  const int4 none = make_int4(0, 0, 0, 0);
+  const int c = c0 + warp;
+  int4 mine;
+  // First the rows of sequences without a token, or with a length out of range: nothing
+  // of the split kernel's is needed for them. Once more for all others where a wait ran out.
+  for (bool gave_up = false;; gave_up = true) {
+    for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
+      const int len = a.kv_lens[n];
+      const bool ok = len_ok(a, len);
+      if ((ok && len > 0) != gave_up) continue;
+      const bool nan = !ok || gave_up;
+      for (int i = tid; i < a.Hkv * (D / 4); i += kJoinThreads) {
+        const int hq = i / (D / 4) * p.G + h, d = 4 * (i % (D / 4));
+        const float v = nan ? __int_as_float(0x7fc00000) : 0.f;
+        float y[4] = {v, v, v, v};
+        put_out<4>(a, (int64_t)n * a.Hq + hq, d, load_gate<4>(a, n, hq, d), y);
+        if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = nan ? v : -INFINITY;
+      }
     }
-  }
-  wait_for_previous();
-  let_next_start();
-  if (blockIdx.x == 0 && h == 0) {
+    if (gave_up) return;
+    wait_for_previous();
+    let_next_start();
+    mine = c < ranges ? p.join[c] : none;
+    constexpr int kFlags = (kMaxRanges + kJoinThreads - 1) / kJoinThreads;
     int f = 0;
-    for (int i = tid; i < ranges; i += kJoinThreads) f |= p.flag[i];
-    const int timeout = __syncthreads_or(f & 1), wrong = __syncthreads_or(f & 2);
-    if (tid == 0) *p.status = timeout ? 1 : (wrong ? 2 : 0);
+#pragma unroll
+    for (int i = 0; i < kFlags; ++i)
+      f |= tid + i * kJoinThreads < ranges ? p.flag[tid + i * kJoinThreads] : 0;
+    const bool timeout = __syncthreads_or(f & 1);
+    if (blockIdx.x == 0 && h == 0) {
+      const int wrong = __syncthreads_or(f & 2);
+      if (tid == 0) *p.status = timeout ? 1 : (wrong ? 2 : 0);
+    }
+    if (!timeout) break;
   }
   // one warp's sum over pieces first, first + step, ...; returns the max and sum
   // over all pieces. Loads go out several at a time.
@@ -1016,9 +1073,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
     }
     if (a.lse && lane == 0) a.lse[row] = (ml.x + log2f(ml.y)) * kLn2;
   };
-  const int4 none = make_int4(0, 0, 0, 0);
-  const int c = c0 + warp;
-  const int4 mine = c < ranges ? p.join[c] : none;
   if (lane == 0) entry[warp] = mine;
   const bool many = mine.w && mine.z - c + 1 > kFewPieces;
   float y[K][V];
@@ -1170,6 +1224,8 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a) {
   p.a = a;
   p.G = a.Hq / a.Hkv;
   p.sl2 = a.scale * 1.4426950408889634f;
+  p.limit_ns = wait_limit_ns();
+  p.poll = p.limit_ns < kSuspendNs;
   p.status = reinterpret_cast<int*>(ws);
   p.flag = reinterpret_cast<int*>(ws + 256);
   p.join = reinterpret_cast<int4*>(ws + 256 + kMaxRanges * 4);

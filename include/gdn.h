@@ -212,7 +212,8 @@ gdn_status gdn_chunked_prefill_status(const void* workspace, cudaStream_t stream
  * gdn_set_wait_limit_ns -- the bound, in nanoseconds, on each wait of the
  * chunked prefill kernel for a flag that another CTA sets (0 restores the
  * default, 2 s). A lower bound makes a stuck call give up sooner; the waits of
- * a CTA on its own copies and tensor-core products keep their 2 s bound.
+ * a CTA on its own copies and tensor-core products keep their 2 s bound. It is
+ * also the bound on each wait between the warps of gdn_paged_attention_decode.
  * Process-wide; read at each launch. Additional entry point.
  */
 void gdn_set_wait_limit_ns(uint64_t ns);
@@ -596,8 +597,9 @@ gdn_status gdn_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k,
  * A sequence of length 0 gives a zero row (lse -inf). A length outside [0,
  * max_pages * page_size] or a page outside [0, num_pages) gives NaN there and
  * GDN_ERR_INVALID_ARG from gdn_attention_status(workspace); a bounded wait that
- * ran out gives GDN_ERR_TIMEOUT there (a call with N = 0 leaves that word). H_q / H_kv is at most 16, N at most
- * 65535. Cached rows behind a sequence's end are never used, whatever they
+ * ran out (gdn_set_wait_limit_ns) gives GDN_ERR_TIMEOUT there and NaN in every
+ * row with tokens (a call with N = 0 leaves that word). H_q / H_kv is at most
+ * 16, N at most 65535. Cached rows behind a sequence's end are never used, whatever they
  * hold. The result does not depend on which CTA runs first: equal calls give
  * equal bits.
  */
