@@ -161,7 +161,14 @@ c10::Device one_device(const T*... all) {
   }
   return first->device();
 }
-void* addr(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
+// The address of a tensor's values; null for none. Tensors that only stand for others
+// throw here, or have none, which must not pass for an argument that was left out.
+void* addr(const at::Tensor* t) {
+  if (!t) return nullptr;
+  void* p = t->data_ptr();
+  if (!p && t->numel() > 0) refuse("a tensor without memory");
+  return p;
+}
 const int32_t* ints(const at::Tensor* t) { return static_cast<const int32_t*>(addr(t)); }
 
 // result, or what Python is to raise
@@ -182,7 +189,7 @@ PyObject* guarded(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, F body) 
   return nullptr;
 }
 // the C entry point without the interpreter's lock: a launch can wait for room in the
-// queue. The call must not throw.
+// queue. The call must not throw: addresses are taken before it.
 template <class F>
 gdn_status unlocked(F call) {
   gdn_status st;
@@ -231,15 +238,17 @@ PyObject* page_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
     for (int i = 0; i < 6; ++i) {
       out[i] = given[i] ? *given[i]
                         : at::empty({sizes[i]}, at::TensorOptions().dtype(at::kInt).device(dev));
-      o[i] = static_cast<int32_t*>(out[i].data_ptr());
+      o[i] = static_cast<int32_t*>(addr(&out[i]));
     }
     const int n32 = narrow(N, "lens"), p32 = narrow(P, "free_pages");
+    const int width = (int)table.size(1);
+    const int32_t *lens_p = ints(&lens), *want_p = ints(&want), *count_p = ints(&free_count);
+    int32_t *table_p = static_cast<int32_t*>(addr(&table)),
+            *free_p = static_cast<int32_t*>(addr(&free_pages));
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     const gdn_status st = unlocked([&] {
-      return page_plan_fn(ints(&lens), ints(&want), n32, static_cast<int32_t*>(table.data_ptr()),
-                          row, (int)table.size(1), static_cast<int32_t*>(free_pages.data_ptr()),
-                          ints(&free_count), p32, page, capacity, o[0], o[1], o[2], o[3], o[4],
-                          o[5], stream);
+      return page_plan_fn(lens_p, want_p, n32, table_p, row, width, free_p, count_p, p32, page,
+                          capacity, o[0], o[1], o[2], o[3], o[4], o[5], stream);
     });
     if (st != GDN_OK) return status(st);
     PyObject* r = PyTuple_New(6);
@@ -344,12 +353,15 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int hq = narrow(Hq, "H_q"), hkv = narrow(Hkv, "H_kv"), d = narrow(D, "head_dim"),
               r = narrow(R, "rope_dims"), p = narrow(P, "num_pages"), ps = narrow(page, "page_size");
     const gdn_dtype out_code = code(out_type, "q_out");
+    const void *q_p = addr(q), *k_p = addr(k), *v_p = addr(v), *wq_p = addr(wq), *wk_p = addr(wk);
+    void *out_p = addr(q_out), *kc_p = addr(kc), *vc_p = addr(vc);
+    const int32_t *pos_p = ints(pos), *slots_p = ints(slots);
+    const double* inv_p = static_cast<const double*>(addr(inv));
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     const gdn_status st = unlocked([&] {
-      return norm_rope_fn(addr(q), qs, addr(k), ks, addr(v), vs, xd, addr(wq), addr(wk), wd, eps,
-                          ints(pos), axes, static_cast<const double*>(addr(inv)), r, interleaved,
-                          scale, ints(slots), T, hq, hkv, d, addr(q_out), addr(kc), kstr.page,
-                          kstr.token, kstr.head, addr(vc), vstr.page, vstr.token, vstr.head, p, ps,
+      return norm_rope_fn(q_p, qs, k_p, ks, v_p, vs, xd, wq_p, wk_p, wd, eps, pos_p, axes, inv_p, r,
+                          interleaved, scale, slots_p, T, hq, hkv, d, out_p, kc_p, kstr.page,
+                          kstr.token, kstr.head, vc_p, vstr.page, vstr.token, vstr.head, p, ps,
                           out_code, stream);
     });
     if (st != GDN_OK) return status(st);
@@ -413,13 +425,17 @@ PyObject* paged_attention_decode(PyObject*, PyObject* const* args, Py_ssize_t n)
                           at::TensorOptions().dtype(at::kByte).device(dev));
       ws = &made_ws;
     }
+    const void *q_p = addr(&q), *kc_p = addr(&kc), *vc_p = addr(&vc), *gate_p = addr(gate);
+    void *o_p = addr(o), *ws_p = addr(ws);
+    const int32_t *table_p = ints(&table), *lens_p = ints(&lens);
+    float* lse_p = static_cast<float*>(addr(lse));
+    const int width = (int)table.size(1);
+    const size_t ws_bytes = ws->nbytes();
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     const gdn_status st = unlocked([&] {
-      return decode_fn(q.data_ptr(), qs, kc.data_ptr(), ks.page, ks.token, ks.head, vc.data_ptr(),
-                       vs.page, vs.token, vs.head, kv_code, p, ps, ints(&table), row,
-                       (int)table.size(1), ints(&lens), addr(gate), gs, n32, hq, hkv, d, scale,
-                       o->data_ptr(), od, static_cast<float*>(addr(lse)), ws->data_ptr(),
-                       (size_t)ws->nbytes(), stream);
+      return decode_fn(q_p, qs, kc_p, ks.page, ks.token, ks.head, vc_p, vs.page, vs.token, vs.head,
+                       kv_code, p, ps, table_p, row, width, lens_p, gate_p, gs, n32, hq, hkv, d,
+                       scale, o_p, od, lse_p, ws_p, ws_bytes, stream);
     });
     if (st != GDN_OK) return status(st);
     return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[7]);
