@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <sstream>
@@ -183,8 +184,9 @@ PyObject* guarded(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, F body) 
   } catch (const Refusal& r) {
     PyErr_SetString(r.type, r.text.c_str());
   } catch (const PythonError&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    // torch's own, as torch raises them (out of memory among them), and Python's
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -3,6 +3,7 @@ that the library cannot take. Nothing is launched in these calls."""
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import gated_delta_rule_106_b200 as gdn
 
@@ -54,4 +55,27 @@ def test_tensors_without_an_address(call, names):
         with pytest.raises((ValueError, RuntimeError), match="memory|data pointer|storage"):
             torch.vmap(lambda t: call(dict(s, **{name: t})))(s[name].unsqueeze(0))
     call(state())
+    torch.cuda.synchronize()
+
+
+def test_exceptions_keep_their_types():
+    """Running out of memory for an output, and what a mode raises while one is made."""
+    s = state()
+    try:
+        torch.cuda.set_per_process_memory_fraction(0.005)
+        with pytest.raises(torch.OutOfMemoryError):
+            gdn.gdn_page_plan(s["lens"], s["want"], s["table"], s["free"], s["count"], 16,
+                              token_capacity=1 << 30)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+
+    class Stop(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            raise KeyError("stop")
+
+    for call in (plan, rope, decode):
+        t = dict(s, o=None)
+        with Stop(), pytest.raises(KeyError, match="stop"):
+            call(t)
+    plan(s)
     torch.cuda.synchronize()
