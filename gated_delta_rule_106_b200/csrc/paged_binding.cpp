@@ -225,6 +225,8 @@ PyObject* page_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
       capacity = given[2]->numel();
     }
     if (capacity < 0) refuse("give token_capacity or slot_map");
+    // before outputs of that size are made
+    if (capacity > (int64_t)1 << 30) return status(GDN_ERR_INVALID_ARG);
     dense(&lens, {N}, "lens", at::kInt);
     dense(&want, {N}, "want", at::kInt);
     const int64_t row = rows32(table, N, "block_table");
