@@ -14,6 +14,7 @@ Agnes-3.0-Flash Preview model card, 架构 table (gated RMS-norm).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -572,6 +573,8 @@ def _binding():
 def _on(stream, tensor):
     """Makes `stream` current for the allocations and the launch of a call, so that
     buffers made for it belong to the stream that uses them."""
+    if not isinstance(tensor, torch.Tensor) or not tensor.is_cuda:
+        return contextlib.nullcontext()          # the binding says what is wrong
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=tensor.device)
     if stream.device != tensor.device:

@@ -24,3 +24,25 @@ def test_plan_capacity_is_refused_before_outputs_are_made(lib):
         gdn.gdn_page_plan(i32(3), i32(3), i32(3, 4), i32(9), i32(1), 16,
                           token_capacity=(1 << 30) + 1)
     assert e.value.status == INVALID
+
+
+def test_a_given_stream_does_not_change_refusals():
+    """With a stream the same exceptions as without: missing tensors, wrong types,
+    tensors on the CPU."""
+    q = torch.zeros(5, 8, 64).half()
+    c = torch.zeros(3, 16, 2, 64).half()
+    for kw in ({}, dict(stream=0)):
+        with pytest.raises(ValueError, match="give q"):
+            gdn.gdn_qk_norm_rope(None, None, None, **kw)
+        with pytest.raises(TypeError, match="q: a torch.Tensor is needed"):
+            gdn.gdn_qk_norm_rope([1.0], None, None, **kw)
+        with pytest.raises(TypeError, match="lens: a torch.Tensor is needed"):
+            gdn.gdn_page_plan([3], i32(1), i32(1, 4), i32(9), i32(1), 16, token_capacity=8, **kw)
+        with pytest.raises(TypeError, match="q: a torch.Tensor is needed"):
+            gdn.gdn_paged_attention_decode(None, c, c, i32(5, 2), i32(5), **kw)
+        for call in (lambda: gdn.gdn_qk_norm_rope(q, None, None, **kw),
+                     lambda: gdn.gdn_page_plan(i32(3), i32(3), i32(3, 4), i32(9), i32(1), 16,
+                                               token_capacity=8, **kw),
+                     lambda: gdn.gdn_paged_attention_decode(q, c, c, i32(5, 2), i32(5), **kw)):
+            with pytest.raises(ValueError, match="CUDA tensors only"):
+                call()
