@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "gdn.h"
 #include "gdn_common.cuh"
 #include "launch.h"
@@ -520,6 +522,9 @@ gdn_status gdn_rope_inv_freq(int rope_dims, double base, double factor, double c
   if (rope_dims < 0 || rope_dims % 2 != 0 || rope_dims > 256) return GDN_ERR_UNSUPPORTED;
   if (!(base > 1.0) || !(factor >= 1.0) || !(context >= 0.0) ||
       (context > 0.0 && !(beta_fast > beta_slow)))
+    return GDN_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || !std::isfinite(factor) || !std::isfinite(context) ||
+      (context > 0.0 && !(std::isfinite(beta_fast) && std::isfinite(beta_slow))))
     return GDN_ERR_INVALID_ARG;
   if (rope_dims == 0) return GDN_OK;
   if (!out) return GDN_ERR_INVALID_ARG;

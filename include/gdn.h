@@ -532,7 +532,7 @@ gdn_status gdn_page_plan(const int32_t* lens, const int32_t* want, int N,
  *                 (beta_fast - beta_slow), 0, 1), f_i * (keep + (1 - keep) /
  *                 factor).
  * rope_dims is even and at most 256; base > 1; factor >= 1; beta_fast >
- * beta_slow where context > 0.
+ * beta_slow where context > 0; all of them finite.
  */
 gdn_status gdn_rope_inv_freq(int rope_dims, double base, double factor, double context,
                              double beta_fast, double beta_slow, double* out,

@@ -46,3 +46,17 @@ def test_a_given_stream_does_not_change_refusals():
                      lambda: gdn.gdn_paged_attention_decode(q, c, c, i32(5, 2), i32(5), **kw)):
             with pytest.raises(ValueError, match="CUDA tensors only"):
                 call()
+
+
+def test_rope_frequencies_of_infinite_arguments_are_refused(lib):
+    """An infinite base or bound would give NaN frequencies."""
+    inf = float("inf")
+    call = lambda R=64, base=1e7, f=1.0, ctx=8192.0, hi=32.0, lo=1.0: (  # noqa: E731
+        lib.gdn_rope_inv_freq(R, base, f, ctx, hi, lo, None, None))
+    for kw in (dict(base=inf), dict(f=inf), dict(ctx=inf), dict(hi=inf), dict(lo=-inf),
+               dict(hi=inf, lo=-inf), dict(base=float("nan"))):
+        assert call(**kw) == INVALID, kw
+        # the same without a table to make
+        assert call(R=0, **kw) == INVALID, kw
+    assert call(R=0) == OK
+    assert call(R=0, ctx=0.0, hi=inf) == OK                  # the bounds are not used
