@@ -32,6 +32,25 @@ bool partial_overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a0 < b0 + nb && b0 < a0 + na;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
+struct Extent { const void* p; size_t n; };
+// an output over an input or another output
+template <size_t I, size_t O>
+bool outputs_overlap(const Extent (&in)[I], const Extent (&out)[O]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (const Extent& b : in)
+      if (overlap(out[i].p, out[i].n, b.p, b.n)) return true;
+    for (size_t j = i + 1; j < O; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
 // Checks shared by the prefill and decode recurrences.
 gdn_status check_recurrence(const void* q, const void* k, const void* v,
                             gdn_dtype qkv_dtype, int64_t qs, int64_t ks,
@@ -455,12 +474,6 @@ bool valid_dtype3(gdn_dtype t) { return valid_dtype(t) || t == GDN_F16; }
 bool half_dtype(gdn_dtype t) { return t == GDN_F16 || t == GDN_BF16; }
 bool paged_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
 // a cache and its strides: rows of D values, 16-byte aligned, inside int32 slots
 gdn_status check_cache(const void* base, const gdn::PageStrides& s, int num_pages, int page_size,
                        int D) {
@@ -492,24 +505,18 @@ gdn_status gdn_page_plan(const int32_t* lens, const int32_t* want, int N,
   if (!free_pages || !free_count || !cu_new || !new_count || (token_capacity > 0 && !slot_map))
     return GDN_ERR_INVALID_ARG;
   if (N > 0 && (!lens || !want || !block_table || !new_lens)) return GDN_ERR_INVALID_ARG;
-  const struct { const void* p; size_t n; } in[] = {
-      {lens, (size_t)N * 4}, {want, (size_t)N * 4}, {free_count, 4}},
-      out[] = {{new_lens, (size_t)N * 4}, {cu_new, (size_t)(N + 1) * 4},
-               {slot_map, (size_t)token_capacity * 4}, {positions, (size_t)token_capacity * 4},
-               {new_count, 4}, {info, 16}, {free_pages, (size_t)num_pages * 4},
-               {block_table, N > 0 ? ((size_t)(N - 1) * table_row_stride + max_pages) * 4 : 0}};
+  const Extent in[] = {{lens, (size_t)N * 4}, {want, (size_t)N * 4}, {free_count, 4}};
+  const Extent out[] = {
+      {new_lens, (size_t)N * 4}, {cu_new, (size_t)(N + 1) * 4},
+      {slot_map, (size_t)token_capacity * 4}, {positions, (size_t)token_capacity * 4},
+      {new_count, 4}, {info, 16}, {free_pages, (size_t)num_pages * 4},
+      {block_table, N > 0 ? ((size_t)(N - 1) * table_row_stride + max_pages) * 4 : 0}};
   for (const auto& a : in)
     if (!aligned_to(a.p, 4)) return GDN_ERR_MISALIGNED;
   for (const auto& a : out)
     if (!aligned_to(a.p, 4)) return GDN_ERR_MISALIGNED;
   if (!aligned16(slot_map) || !aligned16(positions)) return GDN_ERR_MISALIGNED;
-  const int outs = (int)(sizeof(out) / sizeof(out[0]));
-  for (int i = 0; i < outs; ++i) {
-    for (const auto& b : in)
-      if (overlap(out[i].p, out[i].n, b.p, b.n)) return GDN_ERR_INVALID_ARG;
-    for (int j = i + 1; j < outs; ++j)
-      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return GDN_ERR_INVALID_ARG;
-  }
+  if (outputs_overlap(in, out)) return GDN_ERR_INVALID_ARG;
   gdn::PagePlanArgs a{lens, want, N, block_table, table_row_stride, max_pages, free_pages,
                       free_count, num_pages, page_size, token_capacity, new_lens, cu_new,
                       slot_map, positions, new_count, info, stream};
@@ -582,6 +589,11 @@ gdn_status gdn_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k,
     const size_t out = (size_t)T * q_row * 2;
     const bool same = q == q_out && x_dtype == out_dtype && q_row_stride == q_row;
     if (!same && overlap(q, in, q_out, out)) return GDN_ERR_INVALID_ARG;
+    const Extent small[] = {{q_norm_w, (size_t)head_dim * wb}, {k_norm_w, (size_t)head_dim * wb},
+                            {positions, rope_dims > 0 ? (size_t)axes * T * 4 : 0},
+                            {inv_freq, (size_t)rope_dims * 4}, {slot_map, (size_t)T * 4}};
+    for (const Extent& e : small)
+      if (overlap(e.p, e.n, q_out, out)) return GDN_ERR_INVALID_ARG;
     if (k) {
       const size_t kn = ((size_t)(T - 1) * k_row_stride + kv_row) * xb;
       const size_t vn = ((size_t)(T - 1) * v_row_stride + kv_row) * xb;
@@ -636,10 +648,14 @@ gdn_status gdn_paged_attention_decode(const void* q, int64_t q_row_stride, const
       (gate && gate_row_stride % 8 != 0) || !aligned16(o) || !aligned16(workspace) ||
       !aligned_to(block_table, 4) || !aligned_to(kv_lens, 4) || !aligned_to(lse, 4))
     return GDN_ERR_MISALIGNED;
-  const size_t o_bytes = (size_t)N * row * gdn::elem_bytes(o_dtype);
-  if (overlap(q, ((size_t)(N - 1) * q_row_stride + row) * 2, o, o_bytes) ||
-      (gate && overlap(gate, ((size_t)(N - 1) * gate_row_stride + row) * 2, o, o_bytes)))
-    return GDN_ERR_INVALID_ARG;
+  const Extent in[] = {{q, ((size_t)(N - 1) * q_row_stride + row) * 2},
+                       {gate, ((size_t)(N - 1) * gate_row_stride + row) * 2},
+                       {kv_lens, (size_t)N * 4},
+                       {block_table, ((size_t)(N - 1) * table_row_stride + max_pages) * 4}};
+  const Extent out[] = {{o, (size_t)N * row * gdn::elem_bytes(o_dtype)},
+                        {lse, (size_t)N * H_q * 4},
+                        {workspace, gdn::paged_decode_workspace(H_q / H_kv, head_dim)}};
+  if (outputs_overlap(in, out)) return GDN_ERR_INVALID_ARG;
   gdn::PagedDecodeArgs a{q, q_row_stride, k_cache, v_cache, ks, vs, kv_dtype, num_pages,
                          page_size, block_table, table_row_stride, max_pages, kv_lens, gate,
                          gate_row_stride, N, H_q, H_kv, head_dim, scale, o, o_dtype, lse,

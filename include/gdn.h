@@ -557,7 +557,7 @@ gdn_status gdn_rope_inv_freq(int rope_dims, double base, double factor, double c
  *              token's rows is read or written. NULL: token t has slot t.
  *              Slots of different tokens must differ.
  *   q_out      [T, H_q, D] contiguous, out_dtype; may be q itself where q is
- *              contiguous and of that type.
+ *              contiguous and of that type, else not over any input.
  *   k_cache, v_cache  out_dtype (GDN_BF16 or GDN_F16) with their strides; not
  *              over q, k, v or q_out.
  * Sums and rotations are in fp32 (angles exact to 2^-31 turns at any int32
@@ -588,12 +588,13 @@ gdn_status gdn_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k,
  *   block_table [N, max_pages] int32, row stride table_row_stride; entries past
  *              a sequence's last page are not read.
  *   gate       [N, H_q, D] bf16 (row stride) or NULL: o_h * sigmoid(gate_h).
- *   o          [N, H_q, D] contiguous, any of the three types; not over q or gate.
+ *   o          [N, H_q, D] contiguous, any of the three types.
  *   lse        [N, H_q] fp32 or NULL: log sum_j exp(scale * q_h . k_j), to join
  *              outputs over parts of a context (the gate not included).
  *   workspace  gdn_paged_attention_decode_workspace(H_q, H_kv, D) bytes, 16-byte
  *              aligned; nothing has to be set before or kept after a call, but
  *              calls whose executions overlap need their own.
+ * o, lse and workspace must not overlap one another or an input.
  * A sequence of length 0 gives a zero row (lse -inf). A length outside [0,
  * max_pages * page_size] or a page outside [0, num_pages) gives NaN there and
  * GDN_ERR_INVALID_ARG from gdn_attention_status(workspace); a bounded wait that

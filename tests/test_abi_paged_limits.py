@@ -60,3 +60,33 @@ def test_rope_frequencies_of_infinite_arguments_are_refused(lib):
         assert call(R=0, **kw) == INVALID, kw
     assert call(R=0) == OK
     assert call(R=0, ctx=0.0, hi=inf) == OK                  # the bounds are not used
+
+
+A = 1 << 40                        # an aligned address that nothing follows
+STEP = 1 << 34
+
+
+def test_outputs_over_other_arguments_are_refused(lib):
+    """The decode writes o and lse while it reads lengths, tables, queries and gates, and
+    its workspace throughout; the append writes q_out while it reads everything else.
+    Returned before any launch: were one of them taken, the addresses would be followed."""
+    need = lib.gdn_paged_attention_decode_workspace(24, 4, 256)
+    base = dict(q=A, qs=24 * 256, kc=A + STEP, kp=65536, kt=1024, kh=256, vc=A + 2 * STEP, vp=65536,
+                vt=1024, vh=256, kd=2, P=64, page=64, table=A + 3 * STEP, row=16, width=16,
+                lens=A + 4 * STEP, gate=A + 5 * STEP, gs=24 * 256, N=4, Hq=24, Hkv=4, D=256,
+                scale=0.0625, o=A + 6 * STEP, od=0, lse=A + 7 * STEP, ws=A + 8 * STEP, wb=need,
+                s=None)
+    o, lse, ws, row = base["o"], base["lse"], base["ws"], 24 * 256 * 2
+    for kw in (dict(table=o), dict(table=o + 4 * row - 4), dict(lens=o), dict(lse=o + 64),
+               dict(ws=o), dict(ws=o + 4 * row - 16), dict(ws=o - need // 16 * 16),
+               dict(q=lse), dict(gate=lse), dict(table=lse), dict(lens=lse), dict(ws=lse),
+               dict(q=ws), dict(gate=ws), dict(table=ws + 16), dict(lens=ws + need // 16 * 16 - 16)):
+        assert lib.gdn_paged_attention_decode(*{**base, **kw}.values()) == INVALID, kw
+    base = dict(q=A, qs=24 * 256, k=A + STEP, ks=1024, v=A + 2 * STEP, vs=1024, xd=0, wq=A + 6 * STEP,
+                wk=A + 7 * STEP, wd=1, eps=1e-6, pos=A + 8 * STEP, axes=3, inv=A + 9 * STEP, R=64,
+                inter=0, rs=1.0, slots=A + 10 * STEP, T=8, Hq=24, Hkv=4, D=256, qo=A + 3 * STEP,
+                kc=A + 4 * STEP, kp=16384, kt=1024, kh=256, vc=A + 5 * STEP, vp=16384, vt=1024,
+                vh=256, P=8, page=16, od=2, s=None)
+    for name in ("wq", "wk", "pos", "inv", "slots"):
+        for at in (base["qo"], base["qo"] + 8 * row - 16):
+            assert lib.gdn_qk_norm_rope(*{**base, name: at}.values()) == INVALID, name
