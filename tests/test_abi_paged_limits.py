@@ -78,7 +78,7 @@ def test_outputs_over_other_arguments_are_refused(lib):
                 s=None)
     o, lse, ws, row = base["o"], base["lse"], base["ws"], 24 * 256 * 2
     for kw in (dict(table=o), dict(table=o + 4 * row - 4), dict(lens=o), dict(lse=o + 64),
-               dict(ws=o), dict(ws=o + 4 * row - 16), dict(ws=o - need // 16 * 16),
+               dict(ws=o), dict(ws=o + 4 * row - 16), dict(ws=o - (need - 16) // 16 * 16),
                dict(q=lse), dict(gate=lse), dict(table=lse), dict(lens=lse), dict(ws=lse),
                dict(q=ws), dict(gate=ws), dict(table=ws + 16), dict(lens=ws + need // 16 * 16 - 16)):
         assert lib.gdn_paged_attention_decode(*{**base, **kw}.values()) == INVALID, kw
