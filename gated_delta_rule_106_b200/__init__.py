@@ -563,6 +563,10 @@ def _binding():
                 f"{path} is missing: build it with "
                 "`python -m gated_delta_rule_106_b200._build` (nvcc, g++)")
         from . import _paged as ext
+        if ext.built_for != torch.__version__:
+            raise RuntimeError(
+                f"{path} was built for torch {ext.built_for}, this is {torch.__version__}: build it "
+                "again with `python -m gated_delta_rule_106_b200._build`")
         ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gdn_page_plan", "gdn_qk_norm_rope", "gdn_paged_attention_decode",
             "gdn_paged_attention_decode_workspace")])

@@ -469,4 +469,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__paged(void) {
+  PyObject* m = PyModule_Create(&module);
+  // the torch it was compiled against; the package compares it with the one it runs on
+  if (m && PyModule_AddStringConstant(m, "built_for", GDN_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
