@@ -149,8 +149,11 @@ __device__ __forceinline__ void do_heads(const NormRopeArgs& p, const Tx* src, T
           for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              // a lane's last pairs may lie behind rope_dims: an infinite value there
+              // must not meet the other's sine of 0
               const float2 c = turns.cs[i], v = x[u][i];
-              x[u][i] = make_float2(v.x * c.x - v.y * c.y, v.y * c.x + v.x * c.y);
+              if (l * 4 + i < half)
+                x[u][i] = make_float2(v.x * c.x - v.y * c.y, v.y * c.x + v.x * c.y);
             }
         }
       } else {
