@@ -561,8 +561,8 @@ gdn_status gdn_rope_inv_freq(int rope_dims, double base, double factor, double c
  *   k_cache, v_cache  out_dtype (GDN_BF16 or GDN_F16) with their strides; not
  *              over q, k, v or q_out.
  * Sums and rotations are in fp32 (angles exact to 2^-31 turns at any int32
- * position), each value is rounded once; finite values past fp16's range become
- * +-65504.
+ * position), each value is rounded once; values past fp16's range, infinite ones
+ * too, become +-65504 (bf16 keeps infinities).
  * A prompt's rows that gdn_attention_prefill returned go into the cache by a
  * call without q, norm weights and rotary.
  */
@@ -600,9 +600,11 @@ gdn_status gdn_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k,
  * GDN_ERR_INVALID_ARG from gdn_attention_status(workspace); a bounded wait that
  * ran out (gdn_set_wait_limit_ns) gives GDN_ERR_TIMEOUT there and NaN in every
  * row with tokens (a call with N = 0 leaves that word). H_q / H_kv is at most
- * 16, N at most 65535. Cached rows behind a sequence's end are never used, whatever they
- * hold. The result does not depend on which CTA runs first: equal calls give
- * equal bits.
+ * 16, N at most 65535. Cached rows behind a sequence's end are never used,
+ * whatever they hold. An infinite value among a sequence's rows makes its dim
+ * infinite or NaN, and so may bf16 values above 2^112 / kv_lens[n] (weights
+ * reach 2^15 and enter in two or three 16-bit parts). The result does not
+ * depend on which CTA runs first: equal calls give equal bits.
  */
 size_t gdn_paged_attention_decode_workspace(int H_q, int H_kv, int head_dim);
 gdn_status gdn_paged_attention_decode(const void* q, int64_t q_row_stride, const void* k_cache,

@@ -92,3 +92,29 @@ def test_weights_keep_their_bits_in_fp32_outputs(D, H_q, H_kv, dtype):
     for _ in range(1 if dtype == F16 else 2):
         left = left - left.to(dtype).double()
     assert float(((left / p).abs() / bound).max()) > 2
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_infinite_and_large_cached_values(dtype):
+    """An infinite value of a row among a sequence's makes its dim infinite or NaN in the
+    heads that share it (a weight enters in parts, high * inf + low * inf: NaN where the
+    low part is not above 0) and nothing else; values up to 2^112 / length of bf16 caches
+    are no different from others."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    N, L, H_q, H_kv, D = 3, 70, 4, 2, 64
+    q, k, v = (torch.randn(*n, D, device=DEV, generator=g).to(dtype)
+               for n in ((N, H_q), (N, L, H_kv), (N, L, H_kv)))
+    args = paged(k, v, 16)
+    clean = gdn.gdn_paged_attention_decode(q, *args, o_dtype=F32)
+    assert bool(clean.isfinite().all())
+    for at in (0, 33, L - 1):
+        w = v.clone()
+        w[1, at, 1, 7] = float("inf")
+        o = gdn.gdn_paged_attention_decode(q, *paged(k, w, 16), o_dtype=F32)
+        hit = torch.zeros_like(o, dtype=torch.bool)
+        hit[1, 2:, 7] = True
+        assert not bool(o[hit].isfinite().any()) and torch.equal(o[~hit], clean[~hit])
+    if dtype == BF16:
+        big = 2.0 ** 100
+        o = gdn.gdn_paged_attention_decode(q, *paged(k, v * big, 16), o_dtype=F32)
+        assert torch.equal(o, clean * big)
