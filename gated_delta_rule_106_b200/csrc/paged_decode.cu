@@ -927,10 +927,12 @@ paged_split_kernel(const __grid_constant__ PagedParams p,
     }
     if (dead) atomicMax(&trouble, 3);           // a wait ran out: more than bad input
   }
-  // the join takes its place on the chip as CTAs end (allowed from the start on, its
-  // blocks wait beside the running ones: up to 2.5 us more)
-  let_next_start();
   __syncthreads();
+  // The join takes its place on the chip as CTAs end. It counts on this standing behind
+  // every thread's wait_for_previous(), and any warp's call would count for the CTA: ahead
+  // of the barrier, where copying warps without work made it at the start of the CTA,
+  // the join's blocks came in beside the running ones (up to 1 us more).
+  let_next_start();
   // nor may copies be in flight when the CTA ends that computing warps gave up waiting for
   if (trouble == 3 && p.box)
     for (int i = max(0, copied - C::kStages); i < copied; ++i)
@@ -960,7 +962,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   const int c = c0 + warp;
   int4 mine;
   // First the rows of sequences without a token, or with a length out of range: nothing
-  // of the split kernel's is needed for them. Once more for all others where a wait ran out.
+  // of the split kernel's is needed for them. This stands ahead of the wait because the
+  // split kernel lets the join start only after its own: what came before both is done.
+  // Once more for all others where a wait ran out.
   for (bool gave_up = false;; gave_up = true) {
     for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
       const int len = a.kv_lens[n];

@@ -3,7 +3,11 @@
 // calls wait_for_previous() before it touches global memory: it returns when the
 // kernels before have completed and their writes are visible. let_next_start()
 // lets a kernel that is launched this way after it come in once every CTA has called
-// it (or ended); any other kernel after it waits for its end as always.
+// it, by any of its threads, or ended; any other kernel after it waits for its end as
+// always. Where a kernel calls it only behind its own wait (paged_split_kernel), the
+// next one may touch before its wait what that one neither reads nor writes
+// (paged_join_kernel's rows without tokens); a kernel that calls it first gives no such
+// promise (page_plan_kernel, qk_norm_rope_kernel).
 #pragma once
 
 #include <cuda_runtime.h>
