@@ -10,8 +10,9 @@
 // product with the integer position, modulo 2^64, is the turn's fraction with
 // an absolute error below |pos| * 2^-55 turns (the double's own rounding), so
 // a position of 10^6 keeps 2^-35 of a turn -- where a 32-bit product
-// pos * inv_freq is off by 2^-5 of a radian already. cos and sin then need 32
-// bits only.
+// pos * inv_freq is off by 2^-5 of a radian already. Its top 32 bits go to fp32, which
+// keeps 24 of them: another 2^-26 turns at most (10^-7 of a radian, what cos and sin in
+// fp32 are off by anyway, and far below the outputs' 16 bits).
 //
 // A warp takes a token and a share of its heads (all of them where there are
 // tokens enough to fill the chip). D / 8 lanes hold a row, 8 elements each, so a

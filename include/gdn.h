@@ -560,8 +560,8 @@ gdn_status gdn_rope_inv_freq(int rope_dims, double base, double factor, double c
  *              contiguous and of that type, else not over any input.
  *   k_cache, v_cache  out_dtype (GDN_BF16 or GDN_F16) with their strides; not
  *              over q, k, v or q_out.
- * Sums and rotations are in fp32 (angles exact to 2^-31 turns at any int32
- * position), each value is rounded once; values past fp16's range, infinite ones
+ * Sums and rotations are in fp32 (angles within 2^-26 + |position| * 2^-55 turns
+ * for frequencies up to 1), each value is rounded once; values past fp16's range, infinite ones
  * too, become +-65504 (bf16 keeps infinities).
  * A prompt's rows that gdn_attention_prefill returned go into the cache by a
  * call without q, norm weights and rotary.
