@@ -654,7 +654,8 @@ def gdn_qk_norm_rope(q, k, v, k_cache=None, v_cache=None, *, slot_map=None, q_no
     D] and k [T, H_kv, D], and the append of k and v to the paged caches
     [num_pages, page_size, H_kv, D] (strided views; bf16 or fp16) at slot_map [T]
     (a slot outside the cache marks padding; None: token t at slot t). q, or k
-    and v, may be None. Returns q_out [T, H_q, D] in the caches' dtype."""
+    and v, may be None. Returns q_out [T, H_q, D] in the caches' dtype (without
+    caches in out_dtype, else q_out's dtype, else fp16)."""
     if stream is not None:
         with _on(stream, q if q is not None else k):
             return gdn_qk_norm_rope(

@@ -18,10 +18,16 @@
 // requests are only read, of growing ones only written past their held pages.
 // So a call repeated on the same inputs gives the same outputs.
 //
-// Latency bounds it: 64 requests 6.8 us, 509 with 8192 tokens 9.3, 4096 with room
-// for 262144 tokens 12.6 (2.2 MB; each CTA's sums are most of it), of which a launch
+// Latency bounds it: 64 requests 6.8 us, 509 with 8192 tokens 9.4, 4096 with room
+// for 262144 tokens 13.0 (2.2 MB; each CTA's sums are most of it), of which a launch
 // is 2. Requests read once instead of in each pass, divisions by multiplication
 // and a CTA sized to the step took it there from 8.6, 11.6 and 17.6.
+//
+// Two kinds of step are far from that. The grid goes by the token budget alone: 25
+// requests of 16384 tokens that end (25600 pages) take 112 us with room for 512 tokens,
+// 6.4 with room for 65536. And a token's request is searched once per four tokens and
+// then walked to, past every request that does not grow: of 16384 requests two growing
+// ones at the ends take 482 us, 64 spread ones 90, all of them 59 (of 1024: 31, 8, 5.6).
 #include "gdn_common.cuh"
 #include "launch.h"
 #include "pdl.cuh"

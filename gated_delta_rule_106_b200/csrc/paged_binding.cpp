@@ -1,9 +1,10 @@
 // Python binding of the paged-cache calls: checks the tensors, makes the
 // outputs that were not given and calls the C ABI on the current stream.
 //
-// A serving step makes these calls once per layer, and a small one takes 4 to 10 us on
+// A serving step makes these calls once per layer, and a small one takes 4 to 11 us on
 // the GPU; through ctypes the checks and the 20 to 34 converted arguments took
-// 15, 18 and 30 us on the host, launches included. Here a call takes 5 to 8. Module
+// 15, 18 and 30 us on the host, launches included. Here a call takes 4, 3 and 5.5 with
+// its outputs given, 10 (six of them), 5 and 7.5 with outputs made. Module
 // functions take positional arguments only (the Python functions of the package
 // hold the names, defaults and documentation) and return the result, or the
 // gdn_status as an int where the C entry point refused the call.

@@ -4,9 +4,10 @@
 //
 // The K and V rows cross HBM once, so bytes bound it (2 * G FLOP per cached
 // byte for a group of G query heads, a few percent of the tensor rate): 256
-// sequences of 4097 tokens (24 / 4 heads, D = 256, 4.3 GB) take 616 us, 7.0 TB/s,
-// and 675 us where the power cap holds the clocks at 1.6 GHz; one sequence of
-// 131071 tokens 88 us, 6.1 TB/s.
+// sequences of 4097 tokens (24 / 4 heads, D = 256, 4.3 GB) take 665 to 685 us, 6.4
+// TB/s, call after call, when the power cap holds the clocks at 1.6 GHz, and 630 us,
+// 6.8 TB/s, for the first 50 ms after a pause; one sequence of 131071 tokens 88 us,
+// 6.1 TB/s.
 //
 // The work is cut evenly: the units are (sequence, key-value head, block of 64 or
 // 128 tokens) in that order, and CTAs take ranges of units whatever sequences
@@ -22,10 +23,11 @@
 // cp.async to the same places. What was measured on the way (256 x 4097 tokens):
 // row-sized cp.async.bulk 2.07 ms (a warp's lanes issue them one after the other,
 // ~70 cycles each), cp.async by two warps 0.80, by four 0.64 (0.80 under the power
-// cap: the copies' instructions cost energy), TMA 0.62 (0.68).
+// cap: the copies' instructions cost energy), TMA 0.63 (0.67).
 //
 // Four warps compute, 16-token tiles, on mma.sync m16n8k16 (the legacy warp MMA: a
-// tcgen05 tile of 128 rows would be mostly empty, and the tensor pipe is 8 % busy):
+// tcgen05 tile of 128 rows would be mostly empty, and the tensor pipe is busy in 15 % of
+// the cycles at D = 256, 24 / 4 heads):
 //   S^T = K Q^T   (16 tokens x 8 heads), then
 //   O^T += V^T P^T (D x 8 heads), P^T turned in registers by movmatrix.
 // Tokens or head dims fill the 16 rows and the group's heads the 8 columns, so
@@ -33,7 +35,7 @@
 // the running max) and sum in fp32 and rescales rarely (kTop below).
 // P goes in as high and low 16-bit parts: what rounding it once would cost
 // (2^-9 relative for bf16) is as much as the output's own rounding, and the
-// tensor pipe has room (2 % of the time). For fp32 outputs bf16 takes a third part
+// tensor pipe has room. For fp32 outputs bf16 takes a third part
 // (1.3e-6 of the output without it, 1e-7 with it). The warps' pieces of a sequence
 // meet in the block's own shared memory at its end. Sequences cut between ranges
 // leave un-normalised pieces (max, sum, O) in the workspace; a second small kernel
@@ -1171,12 +1173,16 @@ cudaError_t launch_split(PagedParams p, int sms) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   p.base = min(sms * C::kCtasPerSm, max_ranges(D) / kPhases);
-  // ranges to take over only where the tables have room for enough units
+  // ranges to take over only where the tables have room for enough units (the lengths
+  // are not known here: under a table far wider than they are the CTAs past the base find
+  // one phase and have to be cancelled; 8 short sequences with rows for 131072 tokens
+  // 11.8 us, for 300 10.9)
   const int64_t cap = (int64_t)p.a.max_pages * p.a.page_size;
   const int64_t most = (cap + C::kTok - 1) / C::kTok * p.a.N * p.a.Hkv;
   const int grid = most >= kStealUnits * (int64_t)p.base ? kPhases * p.base : p.base;
   // copies by TMA where the page size has a factor of 8 rows, 16 at D = 256. Against
-  // cp.async: 256 x 4097 tokens, D = 256, pages of 64: 616 us, 666; 64 x 4097, pages of
+  // cp.async, one after the other on one box before the power cap bit: 256 x 4097
+  // tokens, D = 256, pages of 64: 616 us, 666; 64 x 4097, pages of
   // 16: D = 256 168, 180, D = 128 166, 169, D = 64 182, 193; pages of 8: 191, 180;
   // 171, 169; 175, 192
   CUtensorMap k_map{}, v_map{};

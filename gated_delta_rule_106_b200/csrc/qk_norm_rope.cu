@@ -21,11 +21,13 @@
 // There is no barrier. The share's rows are called into L2 before the angles are
 // made.
 //
-// Bytes bound it at length (32768 tokens of 24 / 4 heads of 256: 186 us, 5.8 TB/s,
-// 88 % of the copy rate), half issue and half the latency of few long warps at 8192
-// (56 us for 41 us of bytes); a step of 64 tokens takes 3.9 us. A CTA per four tokens
-// with angles and rows in shared memory took 130 us at 8192, one kernel for all
-// layouts 63 (see Partner).
+// Bytes bound it at length (32768 tokens of 24 / 4 heads of 256: 186 to 197 us, 5.5 to
+// 5.8 TB/s, 83 to 88 % of the copy rate; through shared memory, R = 20, 242 us), issue
+// (48 % of the cycles) and the latency of its loads at 8192 (56 us for 41 us of bytes:
+// 2.8 waves of warps, 20 per SM at 96 registers); a step of 64 tokens takes 3.9 us. A
+// CTA per four tokens with angles and rows in shared memory took 130 us at 8192, one
+// kernel for all layouts 63 (see Partner). With 16-bit inputs and D = 256 the kLane
+// kernel spills one register.
 #include "gdn_common.cuh"
 #include "launch.h"
 #include "pdl.cuh"
