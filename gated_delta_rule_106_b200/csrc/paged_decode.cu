@@ -314,7 +314,7 @@ __device__ __forceinline__ Gate<V> load_gate(const PagedDecodeArgs& a, int n, in
     const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(
         static_cast<const __nv_bfloat16*>(a.gate) + n * a.gate_row_stride + (int64_t)h * a.D + d);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) g.v[i] = src[i];
+    for (int i = 0; i < V / 2; ++i) g.v[i] = __ldcg(src + i);   // read once, see the join
   }
   return g;
 }
@@ -965,11 +965,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   int4 mine;
   // First the rows of sequences without a token, or with a length out of range: nothing
   // of the split kernel's is needed for them. This stands ahead of the wait because the
-  // split kernel lets the join start only after its own: what came before both is done.
-  // Once more for all others where a wait ran out.
+  // split kernel lets the join start only after its own: what came before both is done,
+  // and read from L2, where it is (a line of this SM's L1 may be older). Once more for
+  // all others where a wait ran out.
   for (bool gave_up = false;; gave_up = true) {
     for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
-      const int len = a.kv_lens[n];
+      int len;
+      asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(len) : "l"(a.kv_lens + n) : "memory");
       const bool ok = len_ok(a, len);
       if ((ok && len > 0) != gave_up) continue;
       const bool nan = !ok || gave_up;
