@@ -969,18 +969,24 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
   // and read from L2, where it is (a line of this SM's L1 may be older). Once more for
   // all others where a wait ran out.
   for (bool gave_up = false;; gave_up = true) {
-    for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
-      int len;
-      asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(len) : "l"(a.kv_lens + n) : "memory");
+    for (int n0 = blockIdx.x; n0 < a.N; n0 += 32 * gridDim.x) {   // 32 lengths at a time
+      int len = 1;
+      const int at = n0 + lane * gridDim.x;
+      if (at < a.N)
+        asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(len) : "l"(a.kv_lens + at)
+                     : "memory");
       const bool ok = len_ok(a, len);
-      if ((ok && len > 0) != gave_up) continue;
-      const bool nan = !ok || gave_up;
-      for (int i = tid; i < a.Hkv * (D / 4); i += kJoinThreads) {
-        const int hq = i / (D / 4) * p.G + h, d = 4 * (i % (D / 4));
-        const float v = nan ? __int_as_float(0x7fc00000) : 0.f;
-        float y[4] = {v, v, v, v};
-        put_out<4>(a, (int64_t)n * a.Hq + hq, d, load_gate<4>(a, n, hq, d), y);
-        if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = nan ? v : -INFINITY;
+      uint32_t todo = __ballot_sync(0xffffffffu, at < a.N && (ok && len > 0) == gave_up);
+      for (; todo; todo &= todo - 1) {
+        const int k = __ffs(todo) - 1, n = n0 + k * gridDim.x;
+        const bool nan = gave_up || !__shfl_sync(0xffffffffu, ok, k);
+        for (int i = tid; i < a.Hkv * (D / 4); i += kJoinThreads) {
+          const int hq = i / (D / 4) * p.G + h, d = 4 * (i % (D / 4));
+          const float v = nan ? __int_as_float(0x7fc00000) : 0.f;
+          float y[4] = {v, v, v, v};
+          put_out<4>(a, (int64_t)n * a.Hq + hq, d, load_gate<4>(a, n, hq, d), y);
+          if (a.lse && d == 0) a.lse[(int64_t)n * a.Hq + hq] = nan ? v : -INFINITY;
+        }
       }
     }
     if (gave_up) return;
