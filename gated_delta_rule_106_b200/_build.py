@@ -92,13 +92,16 @@ def _build_binding(verbose):
     if not _stale(BINDING, [src, os.path.join(INCLUDE, "gdn.h"), __file__]):
         if os.path.exists(stamp) and open(stamp).read() == made:
             return
-    for old in (BINDING, stamp):              # of another torch, or of other sources
-        if os.path.exists(old):
-            os.remove(old)
     tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run(_binding_command() + ["-o", tmp], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(_binding_command() + ["-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    except Exception:
+        for old in (BINDING, stamp):          # of another torch, or of other sources
+            if os.path.exists(old):
+                os.remove(old)
+        raise
     if verbose and (r.stdout or r.stderr):
         sys.stderr.write(r.stdout + r.stderr)
     os.replace(tmp, BINDING)

@@ -21,11 +21,14 @@ def elsewhere(monkeypatch, tmp_path):
 
 def test_library_is_built_where_the_extension_cannot_be(elsewhere, monkeypatch):
     which = _build.shutil.which
-    monkeypatch.setattr(_build.shutil, "which",
-                        lambda name: "/bin/false" if name == "g++" else which(name))
-    with pytest.warns(RuntimeWarning, match="paged-cache calls will raise"):
-        assert _build.build() == gdn.library_path()
-    assert not os.path.exists(_build.BINDING)
+    for compiler in ("/bin/false", "/nowhere/g++"):
+        monkeypatch.setattr(_build.shutil, "which",
+                            lambda name: compiler if name == "g++" else which(name))
+        with open(_build.BINDING, "w") as f:      # an older one must not stay
+            f.write("of another torch")
+        with pytest.warns(RuntimeWarning, match="paged-cache calls will raise"):
+            assert _build.build() == gdn.library_path()
+        assert not os.path.exists(_build.BINDING)
 
 
 def fake_compiler(folder):
