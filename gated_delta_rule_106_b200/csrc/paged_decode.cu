@@ -66,9 +66,10 @@ constexpr int kAhead = 8;                   // blocks that table entries are cal
 // rest's of 10^5 keys with weights of 2^-20 each needs that.
 constexpr float kLift = 11.f, kTop = 15.f;
 // Waits of warps for one another have the caller's bound (gdn_set_wait_limit_ns); at
-// the end of a CTA that gave up, what is still in flight into its shared memory is
-// waited for this long.
-constexpr uint64_t kDrainNs = 2000000000ull;
+// the end of a CTA that gave up, each stage that may still be written to is waited for
+// this long. A copy lands in microseconds; the time passes in full where another warp
+// never came to the stage.
+constexpr uint64_t kDrainNs = 50000000ull;
 constexpr uint64_t kSuspendNs = 1000000ull;
 
 template <int D, int NT>

@@ -20,8 +20,10 @@ DEV = "cuda"
 @pytest.mark.parametrize("D,H_q,H_kv,page,dtype,N,hi", [
     (256, 24, 4, 64, torch.float16, 6, 900),        # copied by TMA
     (128, 8, 4, 7, torch.bfloat16, 5, 700),         # by cp.async
-    (64, 16, 16, 48, torch.float16, 61, 2900),      # ranges that other CTAs take over
-    (256, 8, 4, 16, torch.float16, 40, 4300)])
+    (64, 16, 16, 48, torch.float16, 61, 2900),      # CTAs without work, to be cancelled
+    (256, 8, 4, 16, torch.float16, 40, 4300),
+    (256, 8, 4, 16, torch.float16, 64, 4300),       # ranges that other CTAs take over
+    (128, 16, 8, 9, torch.bfloat16, 64, 4300)])     # the same by cp.async
 def test_waits_that_run_out(D, H_q, H_kv, page, dtype, N, hi):
     g = torch.Generator(device=DEV).manual_seed(D + page)
     width = -(-hi // page)
@@ -63,7 +65,26 @@ def test_waits_that_run_out(D, H_q, H_kv, page, dtype, N, hi):
             assert not bool(o[1].any()) and bool((lse[1] == float("-inf")).all())
     finally:
         gdn.gdn_set_wait_limit_ns(0)
+    def same(o, lse):
+        return (torch.equal(o.nan_to_num(9.0), o_ref.nan_to_num(9.0)) and
+                torch.equal(lse.nan_to_num(9.0, neginf=8.0), lse_ref.nan_to_num(9.0, neginf=8.0)))
+
     o, lse, st = run(ws)
-    assert st == -1
-    assert torch.equal(o[with_tokens].nan_to_num(9.0), o_ref[with_tokens].nan_to_num(9.0))
-    assert torch.equal(lse.nan_to_num(9.0, neginf=8.0), lse_ref.nan_to_num(9.0, neginf=8.0))
+    assert st == -1 and same(o, lse)
+    # bounds that some waits keep and others do not: all or nothing
+    try:
+        for ns in (300, 1000, 2000, 4000, 8000, 16000, 64000, 500000):
+            gdn.gdn_set_wait_limit_ns(ns)
+            for fill in (255, 0, None):
+                if fill is not None:
+                    ws[:need] = fill
+                o, lse, st = run(ws)
+                if st == gdn.GDN_ERR_TIMEOUT:
+                    assert bool(o[with_tokens].isnan().all() and lse[with_tokens].isnan().all())
+                    assert not bool(o[1].any()) and bool((lse[1] == float("-inf")).all())
+                else:
+                    assert st == -1 and same(o, lse), ns
+    finally:
+        gdn.gdn_set_wait_limit_ns(0)
+    o, lse, st = run(ws)
+    assert st == -1 and same(o, lse)
