@@ -5,9 +5,9 @@
 // The K and V rows cross HBM once, so bytes bound it (2 * G FLOP per cached
 // byte for a group of G query heads, a few percent of the tensor rate): 256
 // sequences of 4097 tokens (24 / 4 heads, D = 256, 4.3 GB) take 665 to 685 us, 6.4
-// TB/s, call after call, when the power cap holds the clocks at 1.6 GHz, and 630 us,
-// 6.8 TB/s, for the first 50 ms after a pause; one sequence of 131071 tokens 88 us,
-// 6.1 TB/s.
+// TB/s, call after call on most boxes, where the power cap holds the clocks at 1.6 GHz,
+// and 625 to 630 us, 6.9 TB/s, on one that kept them and elsewhere for the first 50 ms
+// after a pause; one sequence of 131071 tokens 88 us, 6.1 TB/s.
 //
 // The work is cut evenly: the units are (sequence, key-value head, block of 64 or
 // 128 tokens) in that order, and CTAs take ranges of units whatever sequences
