@@ -5,7 +5,7 @@
 // The K and V rows cross HBM once, so bytes bound it (2 * G FLOP per cached
 // byte for a group of G query heads, a few percent of the tensor rate): 256
 // sequences of 4097 tokens (24 / 4 heads, D = 256, 4.3 GB) take 665 to 685 us, 6.4
-// TB/s, call after call on most boxes, where the power cap holds the clocks at 1.6 GHz,
+// TB/s, call after call on most B200s, where the power cap holds the clocks at 1.6 GHz,
 // and 625 to 630 us, 6.9 TB/s, on one that kept them and elsewhere for the first 50 ms
 // after a pause; one sequence of 131071 tokens 88 us, 6.1 TB/s.
 //
@@ -1190,7 +1190,7 @@ cudaError_t launch_split(PagedParams p, int sms) {
   const int64_t most = (cap + C::kTok - 1) / C::kTok * p.a.N * p.a.Hkv;
   const int grid = most >= kStealUnits * (int64_t)p.base ? kPhases * p.base : p.base;
   // copies by TMA where the page size has a factor of 8 rows, 16 at D = 256. Against
-  // cp.async, one after the other on one box before the power cap bit: 256 x 4097
+  // cp.async, one after the other on one B200 before the power cap bit: 256 x 4097
   // tokens, D = 256, pages of 64: 616 us, 666; 64 x 4097, pages of
   // 16: D = 256 168, 180, D = 128 166, 169, D = 64 182, 193; pages of 8: 191, 180;
   // 171, 169; 175, 192
